@@ -7,7 +7,8 @@ functions raises.
 
 Names mirror the C entry points: ``q2k_bytes``, ``expert_bytes``,
 ``quantize_q2k``, ``dequantize_q2k``, ``workspace_bytes``, ``layer``,
-``layer_hostio``, ``stack``, ``sync_status``.
+``layer_hostio``, ``stack``, ``sync_status``; and for a serving step around
+the layer ``page_map``, ``kv_append``, ``paged_attention``, ``verify_drafts``.
 """
 from __future__ import annotations
 
@@ -20,7 +21,7 @@ LIB_PATH = os.path.join(PKG, "libds_moe.so")
 
 DS_OK, DS_ERR_INVALID_ARG, DS_ERR_UNSUPPORTED = 0, -1, -2
 DS_ERR_CUDA, DS_ERR_TIMEOUT, DS_ERR_DEVICE_CHECK = -3, -4, -5
-DS_F32, DS_BF16 = 0, 1
+DS_F32, DS_BF16, DS_F16 = 0, 1, 2
 DS_Q2_K, DS_Q4_K = 0, 1
 
 SYMBOLS = ["ds_moe_q2k_bytes", "ds_moe_expert_bytes", "ds_moe_quantize_q2k",
@@ -30,10 +31,14 @@ SYMBOLS = ["ds_moe_q2k_bytes", "ds_moe_expert_bytes", "ds_moe_quantize_q2k",
            "ds_moe_expert_bytes_fmt", "ds_moe_quantize_q4k", "ds_moe_dequantize_q4k",
            "ds_moe_stack_mixed", "ds_moe_layer_resident", "ds_moe_layer_path_resident",
            "ds_moe_cache_create", "ds_moe_cache_destroy", "ds_moe_cache_layer", "ds_moe_cache_record",
-           "ds_moe_cache_slot", "ds_moe_cache_stats"]
+           "ds_moe_cache_slot", "ds_moe_cache_stats", "ds_moe_page_map", "ds_moe_kv_append",
+           "ds_moe_attention_workspace_bytes", "ds_moe_paged_attention", "ds_moe_attention_path",
+           "ds_moe_verify_drafts"]
 
 # ds_moe_layer_path results
 PATH_NONE, PATH_STREAM, PATH_DECODE3, PATH_GROUPED_GEMV, PATH_TENSOR_CORE, PATH_BATCHED_DECODE = 0, 1, 2, 3, 4, 5
+# ds_moe_attention_path results
+ATTN_GENERIC, ATTN_DECODE, ATTN_CHUNK = 0, 1, 2
 
 
 class DsMoeError(RuntimeError):
@@ -65,6 +70,17 @@ class Debug(ctypes.Structure):
     _fields_ = [("logits", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("w", ctypes.c_void_p),
                 ("counts", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
                 ("perm", ctypes.c_void_p)]
+
+
+class AttnShapeC(ctypes.Structure):
+    _fields_ = [("n_head", ctypes.c_int32), ("n_head_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("window", ctypes.c_int32)]
+
+
+class KVCacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -138,6 +154,20 @@ def load(path: str):
     L.ds_moe_cache_slot.argtypes = [vp, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)]
     L.ds_moe_cache_stats.restype = ctypes.c_int
     L.ds_moe_cache_stats.argtypes = [vp, ctypes.POINTER(i64), ctypes.POINTER(i64), ctypes.POINTER(i64)]
+    i32, ash, kvc = ctypes.c_int32, ctypes.POINTER(AttnShapeC), ctypes.POINTER(KVCacheC)
+    L.ds_moe_page_map.restype = ctypes.c_int
+    L.ds_moe_page_map.argtypes = [vp, vp, i32, i32, vp, i32, vp, i32, i64, vp, vp, i32, vp, vp, vp, vp, cp, sz]
+    L.ds_moe_kv_append.restype = ctypes.c_int
+    L.ds_moe_kv_append.argtypes = [ash, kvc, vp, vp, i64, i64, vp, i64, vp, cp, sz]
+    L.ds_moe_attention_workspace_bytes.restype = ctypes.c_int
+    L.ds_moe_attention_workspace_bytes.argtypes = [ash, i32, i64, i32, ctypes.POINTER(sz), cp, sz]
+    L.ds_moe_paged_attention.restype = ctypes.c_int
+    L.ds_moe_paged_attention.argtypes = [ash, kvc, vp, i32, i64, vp, i64, i64, vp, vp, i32, i32, vp, i64, vp, vp, sz,
+                                         vp, cp, sz]
+    L.ds_moe_attention_path.restype = ctypes.c_int
+    L.ds_moe_attention_path.argtypes = [ash, kvc, vp, i64, i32]
+    L.ds_moe_verify_drafts.restype = ctypes.c_int
+    L.ds_moe_verify_drafts.argtypes = [vp, i64, vp, i64, i32, i64, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, cp, sz]
     return L
 
 
@@ -380,3 +410,150 @@ def stack(shape: MoEShape, layers, x, workspace, eps: float = 1e-6, stream=None,
 def sync_status(stream=None):
     """Synchronise the stream and raise on a recorded device-side error."""
     _call(lib().ds_moe_sync_status, _stream(stream))
+
+
+# ------------------------------------------------ one serving step around the layer
+
+
+@dataclass(frozen=True)
+class AttentionShape:
+    """Heads, types and masks of an attention (ds_moe_attn_shape)."""
+    n_head: int
+    n_head_kv: int
+    head_dim: int
+    page_size: int
+    dtype: int = DS_BF16  # or DS_F16
+    scale: float = 0.0    # 0: 1 / sqrt(head_dim)
+    window: int = 0       # 0: every key up to the token
+
+    def __post_init__(self):
+        c = AttnShapeC(self.n_head, self.n_head_kv, self.head_dim, self.page_size, self.dtype, self.scale, self.window)
+        object.__setattr__(self, "_c", ctypes.byref(c))
+
+
+class KVCache:
+    """Pages of keys and values: k and v are device tensors [pages][page rows][heads][head_dim]
+    of 16-bit elements and the same strides, which may be views in any order with a dense last axis
+    (for instance ``kv[:, 0].transpose(1, 2)`` of pages [2][heads][rows][head_dim])."""
+
+    def __init__(self, k, v):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v: [pages][page rows][heads][head_dim] of the same strides, the last axis dense")
+        if k.element_size() != 2 or k.dtype != v.dtype or not (k.is_cuda and v.is_cuda):
+            raise ValueError("k and v: 16-bit elements of one type on the device")
+        self.k, self.v, self.rows, self.heads, self.dim = k, v, k.shape[1], k.shape[2], k.shape[3]
+        c = KVCacheC(k.data_ptr(), v.data_ptr(), k.shape[0], k.stride(0), k.stride(1), k.stride(2))
+        self._c = ctypes.byref(c)
+
+    def _fits(self, shape: AttentionShape):
+        if self.rows != shape.page_size or self.heads != shape.n_head_kv or self.dim != shape.head_dim:
+            raise ValueError("the cache's pages, heads or head_dim are not the shape's")
+        _half(self.k, shape, "the cache")
+
+
+def _half(t, shape, name):
+    import torch
+    # 16-bit integers are taken as the bits of the shape's type, as everywhere in this binding
+    if t.dtype != torch.int16 and t.dtype != (torch.float16 if shape.dtype == DS_F16 else torch.bfloat16):
+        raise ValueError(f"{name}: another type than the shape's")
+
+
+def _array(t, name, bits, n=None):
+    """Address of a dense device array of `bits`-bit elements, n of them at least."""
+    if not t.is_cuda or t.element_size() * 8 != bits or not t.is_contiguous() or (n is not None and t.numel() < n):
+        raise ValueError(f"{name}: need a dense device tensor of {bits}-bit elements"
+                         + ("" if n is None else f", {n} or more"))
+    return t.data_ptr()
+
+
+def _table(t):
+    if t.dim() != 2 or not t.is_cuda or t.element_size() != 4 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("block_table: need a device int32 tensor [requests][pages], rows dense")
+    return t.data_ptr(), t.shape[1], t.stride(0)
+
+
+def page_map(context_lens, new_lens, free_pages, block_table, page_size: int, slots, positions, cu_new, seq_lens,
+             n_taken, stream=None):
+    """Pages and places of a step's new tokens (ds_moe_page_map): int32 device tensors, slots int64;
+    block_table, slots, positions, cu_new, seq_lens and n_taken are written."""
+    R, cap = context_lens.numel(), slots.numel()
+    table, width, stride = _table(block_table)
+    if block_table.shape[0] < R:
+        raise ValueError("block_table has fewer rows than requests")
+    _call(lib().ds_moe_page_map, _array(context_lens, "context_lens", 32), _array(new_lens, "new_lens", 32, R), R,
+          page_size, _array(free_pages, "free_pages", 32), free_pages.numel(), table, width, stride,
+          _array(slots, "slots", 64), _array(positions, "positions", 32, cap), cap,
+          _array(cu_new, "cu_new", 32, R + 1), _array(seq_lens, "seq_lens", 32, R), _array(n_taken, "n_taken", 32, 1),
+          _stream(stream))
+
+
+def kv_append(shape: AttentionShape, cache: KVCache, k_new, v_new, slots, stream=None):
+    """Copies k_new, v_new [T][n_head_kv][head_dim] (views of any token and head stride) to their slots [T] int64."""
+    cache._fits(shape)
+    _half(k_new, shape, "k_new")
+    if (k_new.shape[1:] != (shape.n_head_kv, shape.head_dim) or k_new.shape != v_new.shape or k_new.stride() != v_new.stride()
+            or (shape.head_dim > 1 and k_new.stride(2) != 1) or k_new.dtype != v_new.dtype or not (k_new.is_cuda and v_new.is_cuda)):
+        raise ValueError("k_new and v_new: device tensors [T][n_head_kv][head_dim] of the same strides, the last axis dense")
+    T = k_new.shape[0]
+    _call(lib().ds_moe_kv_append, shape._c, cache._c, k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0),
+          k_new.stride(1), _array(slots, "slots", 64, T), T, _stream(stream))
+
+
+def attention_workspace_bytes(shape: AttentionShape, n_requests: int, T: int, max_new: int) -> int:
+    n = ctypes.c_size_t(0)
+    _call(lib().ds_moe_attention_workspace_bytes, shape._c, n_requests, T, max_new, ctypes.byref(n))
+    return n.value
+
+
+def _rows(t, shape, name):
+    if (t.shape[1:] != (shape.n_head, shape.head_dim) or not t.is_cuda or (shape.head_dim > 1 and t.stride(2) != 1)
+            or (shape.n_head > 1 and t.stride(1) != shape.head_dim)):
+        raise ValueError(f"{name}: need a device tensor [T][n_head][head_dim] with dense heads")
+    _half(t, shape, name)
+    return t.data_ptr(), t.stride(0)
+
+
+def paged_attention(shape: AttentionShape, cache: KVCache, block_table, q, cu_new, seq_lens, max_new: int, out, workspace,
+                    lse=None, stream=None):
+    """out[T][n_head][head_dim] = attention of the new tokens q over the cache's pages (ds_moe_paged_attention);
+    lse: optional fp32 [T][n_head].  block_table, cu_new and seq_lens as page_map writes them."""
+    cache._fits(shape)
+    R, T = seq_lens.numel(), q.shape[0]
+    qp, qs = _rows(q, shape, "q")
+    op, os_ = _rows(out, shape, "out")
+    table, width, stride = _table(block_table)
+    if block_table.shape[0] < R or out.shape[0] < T:
+        raise ValueError("block_table or out has too few rows")
+    _call(lib().ds_moe_paged_attention, shape._c, cache._c, table, width, stride, qp, qs, T,
+          _array(cu_new, "cu_new", 32, R + 1), _array(seq_lens, "seq_lens", 32), R, max_new, op, os_,
+          None if lse is None else _array(lse, "lse", 32, T * shape.n_head), _array(workspace, "workspace", 8 * workspace.element_size()),
+          workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+def attention_path(shape: AttentionShape, cache: KVCache, q, max_new: int) -> int:
+    """Which kernels paged_attention runs (an ATTN_* value)."""
+    rc = lib().ds_moe_attention_path(shape._c, cache._c, q.data_ptr(), q.stride(0), max_new)
+    if rc < 0:
+        raise DsMoeError(rc, "shape, cache or max_new rejected")
+    return rc
+
+
+def verify_drafts(target, draft, tokens, cu_new, u_accept, u_sample, out_tokens, n_accepted, stream=None):
+    """Checks drafted tokens against target [T][vocab] (fp32 or bf16 probabilities) from given random numbers
+    (ds_moe_verify_drafts).  draft: the drafter's probabilities, rows as target's, or None; out_tokens
+    [requests][max_new] and n_accepted [requests] int32 are written."""
+    import torch
+    if target.dim() != 2 or target.dtype not in (torch.float32, torch.bfloat16) or not target.is_cuda or \
+            (target.shape[1] > 1 and target.stride(1) != 1):
+        raise ValueError("target: need a device tensor [T][vocab] of fp32 or bf16, rows dense")
+    if draft is not None and (draft.shape != target.shape or draft.dtype != target.dtype or not draft.is_cuda or
+                              (draft.shape[1] > 1 and draft.stride(1) != 1)):
+        raise ValueError("draft: need a tensor like target")
+    R, (T, V) = n_accepted.numel(), target.shape
+    if out_tokens.dim() != 2 or out_tokens.shape[0] != R:
+        raise ValueError("out_tokens: need [requests][max_new]")
+    _call(lib().ds_moe_verify_drafts, target.data_ptr(), target.stride(0), _ptr(draft), 0 if draft is None else draft.stride(0),
+          DS_F32 if target.dtype == torch.float32 else DS_BF16, T, V, _array(tokens, "tokens", 32, T),
+          _array(cu_new, "cu_new", 32, R + 1), R, out_tokens.shape[1], _array(u_accept, "u_accept", 32, T),
+          _array(u_sample, "u_sample", 32, R), _array(out_tokens, "out_tokens", 32), _array(n_accepted, "n_accepted", 32),
+          _stream(stream))

@@ -2,8 +2,6 @@
 // argument validation, workspace layout, the per-device status word and the
 // dispatch of one routed MoE layer onto the kernels.
 #include <math.h>
-#include <stdarg.h>
-#include <stdio.h>
 #include <string.h>
 
 #include <algorithm>
@@ -11,6 +9,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "errors.h"
 #include "internal.h"
 
 namespace dsm {
@@ -48,22 +47,6 @@ int device_sms() {
 }
 
 namespace {
-
-int fail(char *err, size_t errlen, int code, const char *fmt, ...) {
-  if (err && errlen) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(err, errlen, fmt, ap);
-    va_end(ap);
-  }
-  return code;
-}
-
-int cuda_fail(char *err, size_t errlen, cudaError_t e, const char *what) {
-  return fail(err, errlen, DS_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 int check_shape(const ds_moe_shape *s, char *err, size_t errlen, Shape *out) {
   if (!s) return fail(err, errlen, DS_ERR_INVALID_ARG, "shape is NULL");
@@ -506,6 +489,12 @@ int ds_moe_sync_status(void *stream, char *err, size_t errlen) {
   if (v & ST_RANGE)
     return fail(err, errlen, DS_ERR_DEVICE_CHECK,
                 "a value beyond the fp16 range reached the tensor-core path and was saturated (status 0x%x)", v);
+  if (v & ST_PAGING)
+    return fail(err, errlen, DS_ERR_DEVICE_CHECK,
+                "a length, slot or page id out of range, or too few free pages or table columns (status 0x%x)", v);
+  if (v & ST_DRAFT)
+    return fail(err, errlen, DS_ERR_DEVICE_CHECK,
+                "a draft outside the vocabulary, or probabilities that cannot be sampled from (status 0x%x)", v);
   if (v) return fail(err, errlen, DS_ERR_DEVICE_CHECK, "device check failed (status 0x%x)", v);
   return DS_OK;
 }
@@ -528,6 +517,6 @@ int ds_moe_layer_path_resident(const ds_moe_shape *shape, int64_t T) {
   return DS_PATH_GROUPED_GEMV;
 }
 
-const char *ds_moe_version(void) { return "ds_moe 0.2 (sm_103a)"; }
+const char *ds_moe_version(void) { return "ds_moe 0.3 (sm_103a)"; }
 
 }  // extern "C"

@@ -1,0 +1,29 @@
+// Launchers of the attention over pages (internal).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace dsm {
+
+struct AttnArgs {
+  const uint16_t *k, *v;
+  int64_t n_pages, ps, rs, hs;  // cache strides in elements: page, row, head
+  const int32_t *table;
+  int width;
+  int64_t table_stride;
+  const uint16_t *q;
+  int64_t qs;
+  const int32_t *cu, *seq;
+  int T, R, max_new;
+  uint16_t *out;
+  int64_t os;
+  float *lse;
+  int H, G, g, D, page, window;  // query heads, key heads, query heads a key head
+  float scale_log2;              // scale * log2(e): the softmax works in powers of two
+  int64_t max_seq;               // keys that the table has columns for
+  unsigned *status;
+};
+
+cudaError_t launch_attention_generic(const AttnArgs &a, bool bf16, cudaStream_t s);
+
+}  // namespace dsm

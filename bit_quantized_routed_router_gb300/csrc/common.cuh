@@ -21,6 +21,8 @@ enum : unsigned {
   ST_TIMEOUT = 1u << 2,       // a bounded device wait expired
   ST_BAD_COUNT = 1u << 3,     // route counts inconsistent
   ST_RANGE = 1u << 4,         // a value beyond the fp16 range met the tensor-core path (saturated)
+  ST_PAGING = 1u << 5,        // a length, slot or page id out of range, or pages or columns ran out
+  ST_DRAFT = 1u << 6,         // a draft outside the vocabulary, or a row without usable probabilities
 };
 
 // Status word address for the current device (set up once per device).

@@ -71,7 +71,11 @@ typedef enum {
   DS_ERR_DEVICE_CHECK = -5  /* a kernel found invalid data                   */
 } ds_status;
 
-typedef enum { DS_F32 = 0, DS_BF16 = 1 } ds_dtype;
+typedef enum {
+  DS_F32 = 0,
+  DS_BF16 = 1,
+  DS_F16 = 2 /* attention and its cache only */
+} ds_dtype;
 
 /* Storage format of the routed experts. */
 typedef enum { DS_Q2_K = 0, DS_Q4_K = 1 } ds_expert_format;
@@ -360,6 +364,156 @@ int ds_moe_layer_path_resident(const ds_moe_shape *shape, int64_t T);
  * Returns DS_OK, DS_ERR_TIMEOUT or DS_ERR_DEVICE_CHECK (with a message
  * naming the check), or DS_ERR_CUDA if the stream itself failed. */
 int ds_moe_sync_status(void *stream, char *err, size_t errlen);
+
+/* ------------------------------------------------------------------------
+ * One serving step around the layer: pages for the new tokens, their keys
+ * and values into the pages, attention over the pages, and the check of
+ * drafted tokens.  (The pages describe the engine's key-value cache and its
+ * speculative decoding only in outline; these entry points are this
+ * library's own.)
+ *
+ * A request r has context_lens[r] tokens whose keys and values are in pages,
+ * and new_lens[r] new ones.  Its key at position j is in page
+ * block_table[r][j / page_size], row j % page_size; a slot is
+ * page * page_size + row.  The new tokens of all requests follow one another
+ * ("ragged"): those of request r are tokens cu_new[r] .. cu_new[r+1]-1, and
+ * its sequence, new tokens included, is seq_lens[r] long.
+ *
+ * Lengths, tables and page ids live on the device, so they are checked there:
+ * what is out of range is reported by ds_moe_sync_status
+ * (DS_ERR_DEVICE_CHECK), and nothing outside the given buffers is read or
+ * written.
+ * ---------------------------------------------------------------------- */
+
+/* Pages and places of a step's new tokens, built on the device.
+ *   context_lens, new_lens  [n_requests] int32 (n_requests 1..16384; 0: no-op
+ *        but for slots, positions, cu_new[0] and n_taken)
+ *   free_pages  [n_free] int32, ids of unused pages
+ *   block_table [n_requests][table_width] int32, rows table_stride apart: the
+ *        first ceil(context/page_size) entries of a row are the request's
+ *        pages; the pages that the new tokens begin are written behind them,
+ *        taken from free_pages in request order.  Other entries are kept.
+ *   slots       [max_tokens] int64 (max_tokens up to 2^24): the slot of each new token, -1 past the
+ *        last (a captured step may have room to spare)
+ *   positions   [max_tokens] int32: its position in its sequence, -1 past the
+ *        last
+ *   cu_new      [n_requests+1] int32, seq_lens [n_requests] int32
+ *   n_taken     [1] int32: pages taken from free_pages
+ * Reported, and still well defined: a length below zero or from 2^30 up
+ * counts as zero; new tokens beyond max_tokens are dropped (cu_new and seq_lens say
+ * so); a page beyond table_width or beyond n_free is none (table entry -1,
+ * where there is one), and the slots of its tokens are -1, as are those in a
+ * held page whose entry is negative.  The inputs are not changed (but for
+ * the table's new entries), so that the same call again gives the same. */
+int ds_moe_page_map(const int32_t *context_lens, const int32_t *new_lens, int32_t n_requests, int32_t page_size,
+                    const int32_t *free_pages, int32_t n_free, int32_t *block_table, int32_t table_width,
+                    int64_t table_stride, int64_t *slots, int32_t *positions, int32_t max_tokens, int32_t *cu_new,
+                    int32_t *seq_lens, int32_t *n_taken, void *stream, char *err, size_t errlen);
+
+/* Heads, types and masks of an attention. */
+typedef struct {
+  int32_t n_head;    /* query heads, a multiple of n_head_kv                  */
+  int32_t n_head_kv; /* key and value heads; query head h reads head
+                        h / (n_head / n_head_kv)                             */
+  int32_t head_dim;  /* 1..128                                               */
+  int32_t page_size; /* tokens a page, 1..65536                              */
+  int32_t dtype;     /* DS_BF16 or DS_F16: q, the cache, the new keys and
+                        values, and out                                      */
+  float scale;       /* multiplies q k^T; 0: 1/sqrt(head_dim)                */
+  int32_t window;    /* keys that a token sees, itself included; 0: all      */
+} ds_moe_attn_shape;
+
+/* Pages of keys and values: element (page, row, head, d) of either is at
+ * page * page_stride + row * row_stride + head * head_stride + d, in
+ * elements, the last axis dense.  Any order of the axes is fine (pages of
+ * rows or of heads; both in one buffer).  The fast kernels want the bases
+ * 16-byte aligned and the strides multiples of 8. */
+typedef struct {
+  void *k, *v;
+  int64_t n_pages;
+  int64_t page_stride, row_stride, head_stride;
+} ds_moe_kv_cache;
+
+/* Copies the keys and values of T tokens to their slots: k_new and v_new
+ * [T][n_head_kv][head_dim], tokens token_stride and heads head_stride
+ * elements apart (so they may be slices of a fused projection).  A slot below
+ * zero is none; one beyond the cache is skipped and reported.  Slots have to
+ * differ from one another. */
+int ds_moe_kv_append(const ds_moe_attn_shape *shape, const ds_moe_kv_cache *cache, const void *k_new,
+                     const void *v_new, int64_t token_stride, int64_t head_stride, const int64_t *slots, int64_t T,
+                     void *stream, char *err, size_t errlen);
+
+/* Device workspace of ds_moe_paged_attention (host call), for up to
+ * n_requests requests, T new tokens and max_new of one request. */
+int ds_moe_attention_workspace_bytes(const ds_moe_attn_shape *shape, int32_t n_requests, int64_t T, int32_t max_new,
+                                     size_t *bytes, char *err, size_t errlen);
+
+/* Attention of each request's new tokens over its pages (its new keys and
+ * values among them: ds_moe_kv_append comes first):
+ *     out = sum_j softmax_j(scale q k_j) v_j over the keys j that the token
+ *           sees: j <= its position, and with a window j > position - window
+ *   q, out      [T][n_head][head_dim], 16-byte aligned or not, tokens
+ *               q_stride / out_stride elements apart (heads dense)
+ *   lse         [T][n_head] fp32 or NULL: log sum_j exp(scale q k_j)
+ *   cu_new, seq_lens, block_table as ds_moe_page_map writes them
+ *   max_new     no request has more new tokens than that (more are reported
+ *               and dropped: their rows of out are not written)
+ * Keys that a token does not see have no influence on it, whatever they or
+ * their values hold (infinities and NaN included).  A token that sees no key
+ * (its sequence is shorter than its chunk) has out 0 and lse -infinity.
+ * Rows of out beyond cu_new[n_requests] are not written.  Sums, maxima and
+ * products are held in fp32; the probabilities are rounded to dtype for the
+ * second product (at most half a unit in the last place each).  A page id
+ * outside the cache counts as a page of zeros, and is reported.
+ * T == 0 or n_requests == 0 is a no-op.  Workspace: 256-byte aligned, scratch.
+ * The result does not depend on the order in which blocks run. */
+int ds_moe_paged_attention(const ds_moe_attn_shape *shape, const ds_moe_kv_cache *cache, const int32_t *block_table,
+                           int32_t table_width, int64_t table_stride, const void *q, int64_t q_stride, int64_t T,
+                           const int32_t *cu_new, const int32_t *seq_lens, int32_t n_requests, int32_t max_new,
+                           void *out, int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                           void *stream, char *err, size_t errlen);
+
+/* Checks drafted tokens against the model's probabilities, from given random
+ * numbers, so that the tokens kept are distributed as the model's own.
+ * Request r was fed tokens[cu_new[r]] (the last one kept) and then its
+ * drafts; row cu_new[r] + i of target and draft is the distribution of the
+ * token behind its i-th, so draft i (from 1) is checked against row
+ * cu_new[r] + i - 1.
+ *   target  [T][vocab], dtype DS_F32 or DS_BF16, rows target_stride elements
+ *           apart: the model's probabilities (any scale: a row is normalised
+ *           by its sum when it is sampled from)
+ *   draft   the same for the drafter (rows of drafts only are read), or NULL:
+ *           the drafter was sure of each draft
+ *   u_accept [T] fp32 (entry of draft i: cu_new[r] + i - 1), u_sample
+ *           [n_requests] fp32, in [0, 1)
+ * Draft x at row i is kept while u_accept * draft(x) < target(x), exactly.
+ * At the first that is not, one token is drawn from max(target - draft, 0)
+ * (from target where that is zero throughout); when all were kept, from the
+ * target row behind the last.  Drawn is the least token whose cumulative sum
+ * exceeds u_sample times the total; the sums are whole numbers of 2^-44, so
+ * they do not depend on any order.
+ *   out_tokens [n_requests][max_new] int32: the drafts kept, the token drawn,
+ *           then -1;  n_accepted [n_requests] int32: drafts kept
+ * A request without new tokens gives -1s and 0.  Reported: a draft outside
+ * the vocabulary (it is not kept), a row that is sampled from and has no
+ * positive probability (token -1), probabilities that are NaN, negative or
+ * above 1 in a row that is sampled from (NaN and negative count as 0, others
+ * as 1), lengths beyond T or max_new (dropped). */
+int ds_moe_verify_drafts(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride,
+                         int32_t dtype, int64_t T, int32_t vocab, const int32_t *tokens, const int32_t *cu_new,
+                         int32_t n_requests, int32_t max_new, const float *u_accept, const float *u_sample,
+                         int32_t *out_tokens, int32_t *n_accepted, void *stream, char *err, size_t errlen);
+
+/* Which kernels ds_moe_paged_attention runs (host call; nothing is
+ * launched): one of the DS_ATTN_* values, or a negative ds_status. */
+enum {
+  DS_ATTN_GENERIC = 0, /* any strides, page and head sizes: CUDA cores        */
+  DS_ATTN_DECODE = 1,  /* few query rows a key head: keys as the rows of the
+                          tensor-core tiles                                  */
+  DS_ATTN_CHUNK = 2    /* many query rows: queries as the rows               */
+};
+int ds_moe_attention_path(const ds_moe_attn_shape *shape, const ds_moe_kv_cache *cache, const void *q,
+                          int64_t q_stride, int32_t max_new);
 
 /* Library version string (static storage). */
 const char *ds_moe_version(void);

@@ -1,0 +1,533 @@
+"""The serving operators on the GPU against their plain 64-bit forms, at the sizes and masks where they can go wrong."""
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_routed_router_gb300 as ds
+import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def shape_of(c):
+    return ds.AttentionShape(c.H, c.G, c.D, c.page, ds.DS_F16 if c.dtype == "f16" else ds.DS_BF16, window=c.window)
+
+
+def attend(c, max_new=None, workspace=None, lse=True, out=None, stream=None):
+    sh, cache = shape_of(c), ds.KVCache(c.k, c.v)
+    max_new = max([1] + c.new) if max_new is None else max_new
+    if workspace is None:
+        workspace = torch.full((ds.attention_workspace_bytes(sh, c.R, c.T, max_new),), 0xFF, dtype=torch.uint8, device="cuda")
+    if out is None:
+        out = torch.full((c.T, c.H, c.D), 7.0, dtype=c.dt, device="cuda")
+    z = torch.full((c.T, c.H), 7.0, device="cuda") if lse else None
+    ds.paged_attention(sh, cache, c.table, c.q, c.cu, c.seq_lens, max_new, out, workspace, lse=z, stream=stream)
+    c.path = ds.attention_path(sh, cache, c.q, max_new)
+    return out, z
+
+
+def check(c, out, lse, rows=None):
+    want, wlse, mag = c.reference()
+    rows = torch.ones(c.T, dtype=torch.bool) if rows is None else rows
+    tol, ltol = c.tolerances(want, mag, c.path != ds.ATTN_GENERIC)
+    off = (out.cpu().double() - want).abs()
+    assert bool((off <= tol)[rows].all()), f"out off by {float((off / tol.clamp(min=1e-30))[rows].max()):.3g} of the tolerance"
+    if lse is not None:
+        got = lse.cpu().double()
+        none = torch.isinf(wlse)
+        assert torch.equal(torch.isneginf(got)[rows], none[rows])
+        assert bool(((got - wlse).abs()[rows] <= ltol + 2.0 ** -24 * wlse.abs()[rows])[~none[rows]].all())
+
+
+R = random.Random(5)
+CASES = {
+    # ctx, new, heads, key heads, dim, page, options
+    "one_key": ([0], [1], 1, 1, 64, 16, {}),
+    "one_token": ([136], [1], 32, 8, 128, 16, {}),
+    "tile_edges": ([126, 127, 128, 255, 256], [1, 1, 1, 1, 1], 8, 2, 128, 32, {}),
+    "some_without_tokens": ([5, 0, 300, 9], [0, 1, 0, 2], 8, 2, 64, 8, {}),
+    "none_cached": ([0, 0, 0], [1, 7, 130], 4, 2, 128, 16, {}),
+    "drafts": (ref.lengths(R, 9, 0, 700), ref.lengths(R, 9, 1, 6), 28, 4, 64, 24, {}),
+    "drafts_f16": (ref.lengths(R, 9, 0, 700), ref.lengths(R, 9, 1, 6), 28, 4, 128, 48, dict(dtype="f16")),
+    "long": ([9000], [1], 8, 1, 128, 16, {}),
+    "long_few_heads": ([20011, 3], [2, 1], 2, 1, 64, 64, {}),
+    "rows_16": ([500], [2], 16, 2, 128, 16, {}),
+    "rows_17": ([500], [17], 1, 1, 128, 16, {}),
+    "rows_64": ([333], [8], 8, 1, 128, 16, {}),
+    "rows_65": ([333], [13], 5, 1, 128, 16, {}),
+    "rows_128": ([200], [16], 8, 1, 64, 16, {}),
+    "rows_129": ([200], [129], 1, 1, 64, 16, {}),
+    "rows_300": ([77], [75], 4, 1, 128, 32, {}),
+    "group_7": ([100, 31], [50, 64], 14, 2, 128, 16, {}),
+    "group_128": ([40], [3], 128, 1, 64, 16, {}),
+    "group_200": ([40], [2], 200, 1, 64, 16, {}),
+    "own_heads": ([64, 200], [90, 33], 6, 6, 64, 48, dict(dtype="f16")),
+    "mixed": ([700, 0, 1, 300, 128], [1, 200, 3, 129, 1], 8, 2, 128, 64, {}),
+    "chunk": ([515], [400], 4, 2, 128, 128, dict(dtype="f16")),
+    "window_1": ([50, 0], [3, 40], 4, 2, 128, 16, dict(window=1)),
+    "window_100": ([500, 40, 0], [3, 300, 140], 4, 2, 128, 16, dict(window=100)),
+    "window_decode": ([1000, 129, 5], [1, 1, 2], 8, 2, 64, 32, dict(window=128)),
+    "window_wide": ([100], [60], 4, 2, 64, 16, dict(window=5000)),
+    "dim_40": ([60, 200], [1, 2], 8, 2, 40, 16, {}),
+    "dim_80": ([60, 200], [70, 2], 8, 2, 80, 8, {}),
+    "dim_96": ([300], [4], 8, 2, 96, 256, {}),
+    "dim_72_f16": ([130], [100], 4, 2, 72, 64, dict(dtype="f16")),
+    "dim_1": ([70], [3], 2, 1, 1, 16, {}),
+    "dim_37": ([70], [3], 2, 1, 37, 16, {}),
+    "page_1": ([70], [3], 4, 2, 64, 1, {}),
+    "page_20": ([170], [3], 4, 2, 64, 20, {}),
+    "page_8": ([170, 1000], [3, 1], 4, 2, 128, 8, {}),
+    "page_40": ([170, 1000], [3, 200], 4, 2, 128, 40, {}),
+    "page_1024": ([170, 1500], [3, 200], 4, 2, 128, 1024, {}),
+    "heads_first": ([170, 1000], [3, 150], 4, 2, 128, 16, dict(layout="heads")),
+    "both_in_one": ([170, 1000], [3, 1], 4, 2, 128, 16, dict(layout="both")),
+    "padded_rows": ([170, 1000], [3, 150], 4, 2, 64, 16, dict(layout="padded")),
+    "odd_strides": ([170, 300], [3, 1], 4, 2, 64, 16, dict(layout="odd")),
+    "fused_q": ([170, 300], [3, 100], 4, 2, 64, 16, dict(qkv=True)),
+    "shorter_than_chunk": ([0, 0], [5, 200], 4, 2, 128, 16, dict(seq=[3, 40])),
+    "empty_sequence": ([0, 30], [5, 1], 4, 2, 128, 16, dict(seq=[0, 31])),
+    "many_requests": (ref.lengths(R, 70, 0, 300), ref.lengths(R, 70, 0, 3), 8, 2, 64, 16, {}),
+    "sharp": ([700], [40], 4, 2, 128, 16, dict(qscale=12.0)),
+    "sharp_decode": ([2000], [2], 4, 2, 128, 16, dict(qscale=12.0, dtype="f16")),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_attention(name):
+    ctx, new, H, G, D, page, kw = CASES[name]
+    c = ref.Case(ctx, new, H, G, D, page, **kw).put()
+    out, lse = attend(c)
+    ds.sync_status()
+    check(c, out, lse)
+    # without lse, and again: the same bits
+    again, _ = attend(c, lse=False)
+    assert torch.equal(out, again)
+
+
+def growing(c, order):
+    """Keys whose scores grow (or fall) along the sequence, so that the running maximum keeps moving (or never does)."""
+    for r, s in enumerate(c.seq):
+        k = torch.zeros(s, c.G, c.D)
+        ramp = torch.arange(s, dtype=torch.float32) / 16
+        k[..., 0] = (ramp if order > 0 else ramp.flip(0))[:, None]
+        c.keys[r] = (k + 0.01 * c.keys[r].float()).to(c.dt)
+    c.q_cpu = (0.1 * c.q_cpu.float()).to(c.dt)
+    c.q_cpu[..., 0] = 8.0
+    return c
+
+
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("new", [1, 4, 150])
+def test_attention_moving_maximum(order, new):
+    c = growing(ref.Case([900, 20], [new, 1], 8, 2, 128, 16), order).put()
+    out, lse = attend(c)
+    ds.sync_status()
+    check(c, out, lse)
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("new", [2, 4, 150, 300])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_later_tokens_have_no_influence(what, new, D):
+    """The last new token's key or value is not a number: rows before it do not see it."""
+    for side in ("values", "keys"):
+        c = ref.Case([120, 40], [new, 3], 8, 2, D, 16)
+        getattr(c, side)[0][-1, :, 3:9] = what
+        c.put()
+        out, lse = attend(c)
+        ds.sync_status()
+        rows = torch.ones(c.T, dtype=torch.bool)
+        rows[new - 1] = False
+        check(c, out, lse, rows)
+        if side == "values":
+            o = out[new - 1, :, 3:9].cpu().double()
+            assert bool((torch.isnan(o) if math.isnan(what) else o == what).all())
+            assert bool(torch.isfinite(out[new - 1, :, 9:]).all()) and bool(torch.isfinite(out[new - 1, :, :3]).all())
+
+
+@pytest.mark.parametrize("new", [1, 3, 150])
+def test_attention_keys_before_the_window_have_no_influence(new):
+    c = ref.Case([400], [new], 4, 2, 128, 16, window=90)
+    first = 400 + 1 - 90
+    c.values[0][:first], c.keys[0][:first] = math.nan, math.inf
+    c.put()
+    out, lse = attend(c)
+    ds.sync_status()
+    check(c, out, lse)
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_attention_bad_page_is_zeros_and_reported(new):
+    for bad in (-1, -(1 << 30), 1 << 30, None):
+        c = ref.Case([200, 50], [new, 1], 4, 2, 128, 16)
+        c.table_cpu_bad = c.n_pages if bad is None else bad
+        c.put()
+        c.table[0, 3] = c.table_cpu_bad
+        c.keys[0][48:64] = 0
+        c.values[0][48:64] = 0
+        out, lse = attend(c)
+        with pytest.raises(ds.DsMoeError) as e:
+            ds.sync_status()
+        assert e.value.code == ds.DS_ERR_DEVICE_CHECK
+        check(c, out, lse)
+    ds.sync_status()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_bad_lengths_are_reported_and_bounded(new):
+    c = ref.Case([100, 90, 80], [new, new, new], 4, 2, 64, 16).put()
+    out0, lse0 = attend(c)
+    ds.sync_status()
+    for name, at, v in (("seq_lens", 1, 1 << 30), ("seq_lens", 1, -5), ("cu", 3, 1 << 20), ("cu", 0, -3)):
+        t = getattr(c, name)
+        keep = int(t[at])
+        t[at] = v
+        out, lse = attend(c)
+        with pytest.raises(ds.DsMoeError) as e:
+            ds.sync_status()
+        assert e.value.code == ds.DS_ERR_DEVICE_CHECK
+        other = slice(0, new) if name == "seq_lens" else slice(new, 2 * new)  # a request that the bad entry is not of
+        assert torch.equal(out[other], out0[other]) and torch.equal(lse[other], lse0[other])
+        t[at] = keep
+    # more new tokens than max_new: dropped, their rows kept as they were
+    if new > 1:
+        out, _ = attend(c, max_new=new - 1)
+        with pytest.raises(ds.DsMoeError):
+            ds.sync_status()
+        assert bool((out[new - 1] == 7.0).all())
+        sh = shape_of(c)
+        if ds.attention_path(sh, ds.KVCache(c.k, c.v), c.q, new - 1) == ds.attention_path(sh, ds.KVCache(c.k, c.v), c.q, new):
+            tol = 2 * torch.finfo(c.dt).eps
+            assert bool(((out[: new - 1] - out0[: new - 1]).abs() <= tol * (1 + out0[: new - 1].abs())).all())
+    ds.sync_status()
+
+
+def test_attention_rows_beyond_the_last_are_kept():
+    c = ref.Case([100, 90], [3, 2], 4, 2, 64, 16).put()
+    c.T += 4
+    c.q = torch.cat([c.q, torch.full((4, 4, 64), math.nan, dtype=c.dt, device="cuda")])
+    out, lse = attend(c)
+    ds.sync_status()
+    assert bool((out[5:] == 7.0).all()) and bool((lse[5:] == 7.0).all())
+    c.T -= 4
+    check(c, out[:5], lse[:5])
+
+
+def test_attention_out_strided_and_in_a_stream_and_a_graph():
+    for new in (2, 150):
+        c = ref.Case([300, 41], [new, 1], 8, 2, 128, 16).put()
+        out0, lse0 = attend(c)
+        sh, cache = shape_of(c), ds.KVCache(c.k, c.v)
+        ws = torch.empty(ds.attention_workspace_bytes(sh, c.R, c.T, new), dtype=torch.uint8, device="cuda")
+        wide = torch.full((c.T, c.H + 3, c.D), 7.0, dtype=c.dt, device="cuda")
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            attend(c, workspace=ws, out=wide[:, : c.H])
+        s.synchronize()
+        assert torch.equal(wide[:, : c.H], out0) and bool((wide[:, c.H:] == 7.0).all())
+        out, lse = torch.empty_like(out0), torch.empty_like(lse0)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ds.paged_attention(sh, cache, c.table, c.q, c.cu, c.seq_lens, new, out, ws, lse=lse)
+        for _ in range(3):
+            out.zero_(), lse.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, out0) and torch.equal(lse, lse0)
+    ds.sync_status()
+
+
+def test_attention_offsets_beyond_32_bits():
+    """Pages whose elements lie beyond 2^31 of the cache's first (and bytes beyond 2^32)."""
+    n_pages, page, G, D = 36000, 64, 8, 128
+    for new in (1, 40):
+        c = ref.Case([500], [new], 16, G, D, page)
+        k, v = (torch.empty(n_pages, page, G, D, dtype=c.dt, device="cuda") for _ in range(2))
+        c.put()
+        used = ref.cdiv(500 + new, page)
+        for j in range(used):
+            k[n_pages - 1 - j], v[n_pages - 1 - j] = c.k[c.table[0, j].long()], c.v[c.table[0, j].long()]
+            c.table[0, j] = n_pages - 1 - j
+        c.k, c.v = k, v
+        out, lse = attend(c)
+        ds.sync_status()
+        check(c, out, lse)
+
+
+@pytest.mark.parametrize("page,D,new,window", [(16, 128, 1, 0), (64, 64, 2, 0), (24, 128, 33, 700)])
+def test_attention_long_sequences(page, D, new, window):
+    """Tens of thousands of keys against a 64-bit form on the device, all heads at once."""
+    H, G, L = 8, 2, 70001
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n = ref.cdiv(L, page)
+    table = torch.randperm(n, generator=g, device="cuda").to(torch.int32).view(1, n)
+    k, v = (torch.randn(n, page, G, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(new, H, D, generator=g, device="cuda").bfloat16()
+    cu = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    seq = torch.tensor([L], dtype=torch.int32, device="cuda")
+    sh = ds.AttentionShape(H, G, D, page, window=window)
+    ws = torch.empty(ds.attention_workspace_bytes(sh, 1, new, new), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(new, H, device="cuda")
+    ds.paged_attention(sh, ds.KVCache(k, v), table, q, cu, seq, new, out, ws, lse=lse)
+    ds.sync_status()
+    kk, vv = (t[table[0].long()].reshape(-1, G, D)[:L].double() for t in (k, v))
+    s = torch.einsum("ighd,jgd->ighj", q.double().view(new, G, H // G, D), kk) / math.sqrt(D)
+    far = torch.arange(L - new, L, device="cuda")[:, None] - torch.arange(L, device="cuda")
+    hidden = (far < 0) | ((far >= window) if window else (far < 0))
+    s = s.masked_fill(hidden[:, None, None], -math.inf)
+    z = torch.logsumexp(s, -1)
+    p = torch.exp(s - z[..., None])
+    want = torch.einsum("ighj,jgd->ighd", p, vv).reshape(new, H, D)
+    mag = torch.einsum("ighj,jgd->ighd", p, vv.abs()).reshape(new, H, D)
+    # a score's fp32 sum: D products of magnitude at most |q||k|; sums of n terms in order are off by at most
+    # (n / 128 + 256) 2^-24 of their magnitude when taken in tiles of 128
+    score = (D + 4) * 2.0 ** -24 * float(q.double().norm(dim=-1).max() * kk.norm(dim=-1).max()) / math.sqrt(D)
+    sums = (L / 128 + 256) * 2.0 ** -24
+    u = 2.0 ** -8
+    tol = u * want.abs() + (u + 2 * score + 2 * sums) * mag
+    assert bool(((out.double() - want).abs() <= tol).all())
+    assert bool(((lse.double() - z.reshape(new, H)).abs() <= score + sums + 2.0 ** -20).all())
+
+
+# -------------------------------------------------------------------- page map
+
+
+def run_page_map(ctx, new, page, free, table, cap):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    R_ = len(ctx)
+    dev = table.cuda()
+    out = dict(slots=torch.full((cap,), 99, dtype=torch.int64, device="cuda"), positions=torch.full((cap,), 99, **i32),
+               cu_new=torch.full((R_ + 1,), 99, **i32), seq_lens=torch.full((R_,), 99, **i32), n_taken=torch.full((1,), 99, **i32))
+    args = (torch.tensor(ctx, **i32), torch.tensor(new, **i32), torch.tensor(free, **i32), dev, page)
+    for _ in range(2):  # the same call again gives the same
+        ds.page_map(*args, **out)
+    try:
+        ds.sync_status()
+        bad = False
+    except ds.DsMoeError as e:
+        assert e.code == ds.DS_ERR_DEVICE_CHECK
+        bad = True
+    return dev.cpu(), {k: v.cpu().tolist() for k, v in out.items()}, bad
+
+
+def held_table(rng, ctx, page, width, n_extra):
+    ids = list(range(sum(ref.cdiv(max(0, c), page) for c in ctx) + n_extra))
+    rng.shuffle(ids)
+    table = torch.full((len(ctx), width), -7, dtype=torch.int32)
+    for r, c in enumerate(ctx):
+        for j in range(min(width, ref.cdiv(max(0, c), page))):
+            table[r, j] = ids.pop()
+    return table, ids
+
+
+@pytest.mark.parametrize("n,ctx_hi,new_hi,page", [(1, 0, 1, 16), (1, 40, 1, 1), (7, 100, 5, 16), (64, 3000, 9, 64), (33, 70, 200, 24),
+                                                  (600, 50, 3, 8), (513, 50, 40, 7), (5, 2, 3000, 100), (3, 5, 0, 16)])
+def test_page_map(n, ctx_hi, new_hi, page):
+    rng = random.Random(n)
+    ctx, new = ref.lengths(rng, n, 0, ctx_hi), ref.lengths(rng, n, 0, new_hi)
+    width = max(1, max(ref.cdiv(a + b, page) for a, b in zip(ctx, new)))
+    table, free = held_table(rng, ctx, page, width, 5 + sum(new))
+    cap = sum(new) + rng.randint(0, 9)
+    got_table, got, bad = run_page_map(ctx, new, page, free, table, cap)
+    slots, positions, cu, seq, taken, want_bad = ref.page_map(ctx, new, page, free, table, cap)
+    assert not bad and not want_bad
+    assert torch.equal(got_table, table)
+    assert got == dict(slots=slots, positions=positions, cu_new=cu, seq_lens=seq, n_taken=[taken])
+
+
+@pytest.mark.parametrize("what", ["few_pages", "no_pages", "narrow", "no_columns", "room", "no_room", "negative", "huge", "hole"])
+def test_page_map_reports(what):
+    rng = random.Random(8)
+    ctx, new = ref.lengths(rng, 9, 0, 50), ref.lengths(rng, 9, 1, 40)
+    width = max(ref.cdiv(a + b, 16) for a, b in zip(ctx, new))
+    cap = sum(new) + 3
+    if what == "narrow":
+        width = 2
+    if what == "negative":
+        ctx[2], new[4], new[5] = -1, -3, -(1 << 31)
+    if what == "huge":
+        ctx[2], new[4] = 1 << 30, (1 << 31) - 1
+    if what == "no_columns":
+        width = 0
+    table, free = held_table(rng, [c if c < 1 << 20 else 0 for c in ctx], 16, width, sum(max(0, v) for v in new if v < 1 << 20))
+    if what == "few_pages":
+        free = free[:4]
+    if what == "no_pages":
+        free = []
+    if what == "room":
+        cap = sum(new) // 2
+    if what == "no_room":
+        cap = 0
+    if what == "hole":
+        ctx[3] = 20
+        table[3, 1] = -1
+    got_table, got, bad = run_page_map(ctx, new, 16, free, table, cap)
+    slots, positions, cu, seq, taken, want_bad = ref.page_map(ctx, new, 16, free, table, cap)
+    assert bad and want_bad
+    assert torch.equal(got_table, table)
+    assert got == dict(slots=slots, positions=positions, cu_new=cu, seq_lens=seq, n_taken=[taken])
+    ds.sync_status()
+
+
+def test_page_map_no_requests_and_many():
+    _, got, bad = run_page_map([], [], 16, [3], torch.zeros(0, 1, dtype=torch.int32), 4)
+    assert not bad and got == dict(slots=[-1] * 4, positions=[-1] * 4, cu_new=[0], seq_lens=[], n_taken=[0])
+    n = 16384
+    rng = random.Random(1)
+    ctx, new = ref.lengths(rng, n, 0, 20), ref.lengths(rng, n, 0, 2)
+    table, free = held_table(rng, ctx, 16, 2, 2 * n)
+    cap = sum(new)
+    got_table, got, bad = run_page_map(ctx, new, 16, free, table, cap)
+    slots, positions, cu, seq, taken, _ = ref.page_map(ctx, new, 16, free, table, cap)
+    assert not bad and torch.equal(got_table, table)
+    assert got == dict(slots=slots, positions=positions, cu_new=cu, seq_lens=seq, n_taken=[taken])
+
+
+# ------------------------------------------------------------------- kv append
+
+
+@pytest.mark.parametrize("T,G,D,page,layout", [(1, 1, 64, 16, "pages"), (37, 8, 128, 16, "pages"), (300, 3, 80, 24, "heads"),
+                                               (65, 2, 37, 5, "pages"), (20, 4, 64, 16, "both"), (20, 4, 64, 16, "odd"),
+                                               (20, 4, 64, 16, "padded"), (3000, 2, 128, 64, "pages")])
+@pytest.mark.parametrize("fused", [False, True])
+def test_kv_append(T, G, D, page, layout, fused):
+    c = ref.Case([T], [1], G, G, D, page, layout=layout).put()
+    g = torch.Generator().manual_seed(T)
+    places = torch.randperm(c.n_pages * page, generator=g)[:T]
+    slots = torch.where(torch.rand(T, generator=g) < 0.2, -1 - places, places) if T > 1 else places
+    if fused:  # slices of one projection
+        kv = torch.randn(T, 2 * G + 1, D, generator=g).to(c.dt).cuda()
+        kn, vn = kv[:, 1: G + 1], kv[:, G + 1:]
+    else:
+        kn, vn = (torch.randn(T, G, D, generator=g).to(c.dt).cuda() for _ in range(2))
+    bits = lambda t: t.cpu().contiguous().view(torch.int16)  # noqa: E731  (NaN are compared too)
+    want = [bits(t).reshape(-1, G, D).clone() for t in (c.k, c.v)]
+    for w, n in zip(want, (kn, vn)):
+        w[slots[slots >= 0]] = bits(n)[slots >= 0]
+    ds.kv_append(shape_of(c), ds.KVCache(c.k, c.v), kn, vn, slots.cuda())
+    ds.sync_status()
+    for t, w in zip((c.k, c.v), want):
+        assert torch.equal(bits(t).reshape(-1, G, D), w)
+    # a slot beyond the cache is skipped and reported
+    slots[0] = c.n_pages * page
+    ds.kv_append(shape_of(c), ds.KVCache(c.k, c.v), kn, vn, slots.cuda())
+    with pytest.raises(ds.DsMoeError) as e:
+        ds.sync_status()
+    assert e.value.code == ds.DS_ERR_DEVICE_CHECK
+    for t, w in zip((c.k, c.v), want):
+        assert torch.equal(bits(t).reshape(-1, G, D), w)
+
+
+# ---------------------------------------------------------------------- verify
+
+
+def run_verify(p, q, tokens, cu, ua, us, max_new, bad=False, pad=0):
+    dev = lambda t: None if t is None else torch.nn.functional.pad(t, (0, pad)).cuda()[:, : t.shape[1]]  # noqa: E731
+    R_ = len(cu) - 1
+    out = torch.full((R_, max_new), 99, dtype=torch.int32, device="cuda")
+    n = torch.full((R_,), 99, dtype=torch.int32, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ds.verify_drafts(dev(p), dev(q), torch.tensor(tokens, **i32), torch.tensor(cu, **i32), torch.tensor(ua, dtype=torch.float32, device="cuda"),
+                     torch.tensor(us, dtype=torch.float32, device="cuda"), out, n)
+    if bad:
+        with pytest.raises(ds.DsMoeError) as e:
+            ds.sync_status()
+        assert e.value.code == ds.DS_ERR_DEVICE_CHECK
+    else:
+        ds.sync_status()
+    return out.cpu().numpy(), n.cpu().numpy()
+
+
+def draws(seed, n_requests, new_lo, new_hi, V, sharp=3.0, dtype=torch.float32, drafted=True):
+    rng = random.Random(seed)
+    g = torch.Generator().manual_seed(seed)
+    new = ref.lengths(rng, n_requests, new_lo, new_hi)
+    cu = [0] + np.cumsum(new).tolist()
+    T = cu[-1]
+    logits = sharp * torch.randn(T, V, generator=g)
+    p = torch.softmax(logits, -1).to(dtype)
+    qf = torch.softmax(logits + torch.randn(T, V, generator=g), -1)
+    tokens = np.roll(torch.multinomial(qf, 1, generator=g)[:, 0].numpy(), 1).astype(np.int32) if T else np.zeros(0, np.int32)
+    ua, us = torch.rand(T, generator=g).numpy(), torch.rand(n_requests, generator=g).numpy()
+    return p, qf.to(dtype) if drafted else None, tokens, cu, ua, us
+
+
+@pytest.mark.parametrize("n,new_lo,new_hi,V", [(1, 1, 1, 1), (1, 4, 4, 5), (7, 0, 4, 33), (20, 1, 6, 1000), (9, 2, 3, 1024), (9, 2, 3, 1025),
+                                               (5, 1, 4, 32768), (40, 1, 8, 100003), (3, 1, 2, 300001), (300, 1, 2, 2049)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("drafted", [True, False])
+def test_verify(n, new_lo, new_hi, V, dtype, drafted):
+    p, q, tokens, cu, ua, us = draws(n + V, n, new_lo, new_hi, V, dtype=dtype, drafted=drafted)
+    mx = new_hi + 1
+    got = run_verify(p, q, tokens, cu, ua, us, mx, pad=3 if V % 2 else 0)
+    want = ref.verify(p.float().numpy(), None if q is None else q.float().numpy(), tokens, cu, ua, us, mx)
+    assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])
+
+
+def test_verify_edges():
+    V = 6
+    p = torch.tensor([[.1, .2, .3, .4, 0, 0], [.25, .25, .25, .25, 0, 0], [0, 0, 0, 0, 0, 1.0]])
+    tok = [0, 3, 1]
+    # u q < p holds strictly: u = 0.5 and p = q / 2 is a refusal; just below is not
+    q = torch.tensor([[.1, .05, .05, .8, 0, 0], [.25, .25, .25, .25, 0, 0], [0, 0, 0, 0, 0, 1.0]])
+    for u, kept in ((.5, 0), (float(np.nextafter(np.float32(.5), np.float32(0))), 2)):
+        out, n = run_verify(p, q, tok, [0, 3], [u, .999, 0], [.5], 3)
+        assert n[0] == kept
+    # draws at both ends of the line, and entries of no weight in between
+    for u, x in ((0.0, 1), (float(np.nextafter(np.float32(1), np.float32(0))), 2)):
+        out, n = run_verify(p, q, tok, [0, 3], [.99, 0, 0], [u], 4)
+        assert n[0] == 0 and out[0].tolist() == [x, -1, -1, -1]
+    # the draft's distribution is the target's: nothing is left at a refusal, so the target itself is drawn from
+    out, n = run_verify(p, p.clone(), [0, 4, 1], [0, 3], [0, 0, 0], [.95], 3)
+    assert n[0] == 0 and out[0].tolist() == [3, -1, -1]
+    # a zero probability of the draft: kept where the target has some
+    out, n = run_verify(p, torch.zeros(3, V), tok, [0, 3], [.9, .9, 0], [.2], 3)
+    assert n[0] == 2 and out[0].tolist() == [3, 1, 5]
+    # a sure drafter: refused, the draft cannot be drawn
+    out, n = run_verify(p, None, [0, 3, 1], [0, 3], [.4, .9, 0], [.9999], 3)
+    assert n[0] == 0 and out[0].tolist() == [2, -1, -1]
+
+
+def test_verify_reports():
+    p, q, tokens, cu, ua, us = draws(4, 6, 3, 3, 700)
+    good = run_verify(p, q, tokens, cu, ua, us, 3)
+    t = tokens.copy()
+    t[cu[2] + 1] = 700                     # a draft that is no token
+    t[cu[4] + 1] = -1
+    out, n = run_verify(p, q, t, cu, ua, us, 3, bad=True)
+    want = ref.verify(p.numpy(), q.numpy(), t, cu, ua, us, 3)
+    assert np.array_equal(out, want[0]) and np.array_equal(n, want[1]) and n[2] == 0 and n[4] == 0
+    for v in (math.nan, -0.25, 2.0):       # a row that is sampled from
+        pp = p.clone()
+        row = cu[3] + int(good[1][3])
+        pp[row, 5] = v
+        out, n = run_verify(pp, q, tokens, cu, ua, us, 3, bad=True)
+        want = ref.verify(pp.numpy(), q.numpy(), tokens, cu, ua, us, 3)
+        assert np.array_equal(out, want[0]) and np.array_equal(n, want[1])
+    pp = p.clone()
+    pp[cu[1] + int(good[1][1])] = 0.0      # nothing to draw from
+    out, n = run_verify(pp, q, tokens, cu, ua, us, 3, bad=True)
+    assert out[1, n[1]] == -1
+    for bad_cu in ([-2, 3, 6, 9, 12, 15, 18], [0, 3, 6, 9, 12, 15, 1 << 20]):
+        run_verify(p, q, tokens, bad_cu, ua, us, 3, bad=True)
+    run_verify(p, q, tokens, cu, ua, us, 2, bad=True)    # more new tokens than out has room for
+    assert np.array_equal(run_verify(p, q, tokens, cu, ua, us, 3)[0], good[0])
+
+
+def test_verify_keeps_the_targets_distribution():
+    """Of many requests with one draft each, the first token kept is distributed as the target (within five standard
+    deviations of a multinomial count)."""
+    n, V = 40000, 7
+    g = torch.Generator().manual_seed(2)
+    p, q = torch.softmax(torch.randn(V, generator=g), -1), torch.softmax(torch.randn(V, generator=g), -1)
+    tokens = torch.zeros(2 * n, dtype=torch.int32)
+    tokens[1::2] = torch.multinomial(q, n, True, generator=g).int()
+    ua, us = torch.rand(2 * n, generator=g).numpy(), torch.rand(n, generator=g).numpy()
+    out, _ = run_verify(p.repeat(2 * n, 1), q.repeat(2 * n, 1), tokens.numpy(), list(range(0, 2 * n + 1, 2)), ua, us, 2)
+    count = np.bincount(out[:, 0], minlength=V)
+    pe = p.double().numpy()
+    assert np.all(np.abs(count - n * pe) <= 5 * np.sqrt(n * pe * (1 - pe)))
