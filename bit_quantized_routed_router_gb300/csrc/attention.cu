@@ -104,6 +104,23 @@ __global__ void __launch_bounds__(GA_WARPS * 32) attention_generic_kernel(const 
   if (bad) flag(a.status, ST_PAGING);
 }
 
+// What the tensor-core kernels' copies need: 16-byte aligned bases, strides
+// and heads, and pages of whole 8-row groups (the swizzle's period).
+bool copies_fit(const ds_moe_attn_shape &s, const ds_moe_kv_cache &c, const void *q, int64_t q_stride, int64_t T) {
+  constexpr int64_t FAR = (int64_t)1 << 39;  // strides of a tensor map are below 2^40 bytes
+  auto fits = [](int64_t n, int64_t stride) { return n <= 1 || (stride > 0 && stride % 8 == 0 && stride < FAR); };
+  return s.head_dim % 8 == 0 && s.page_size % 8 == 0 && s.n_head / s.n_head_kv <= 128 && c.n_pages > 0 &&
+         aligned(c.k, 16) && aligned(c.v, 16) && aligned(q, 16) && fits(s.page_size, c.row_stride) &&
+         fits(s.n_head_kv, c.head_stride) && fits(c.n_pages, c.page_stride) && fits(T, q_stride) && encode_fn() && device_sms();
+}
+
+int path_of(const ds_moe_attn_shape &s, const ds_moe_kv_cache &c, const void *q, int64_t q_stride, int64_t T, int32_t max_new) {
+  if (!copies_fit(s, c, q, q_stride, T)) return DS_ATTN_GENERIC;
+  return (int64_t)max_new * (s.n_head / s.n_head_kv) <= AD_MAX_ROWS ? DS_ATTN_DECODE : DS_ATTN_GENERIC;
+}
+
+int launch_blocks() { return std::max(device_sms(), NUM_SMS); }
+
 }  // namespace
 
 cudaError_t launch_attention_generic(const AttnArgs &a, bool bf16, cudaStream_t s) {
@@ -126,7 +143,7 @@ int ds_moe_attention_path(const ds_moe_attn_shape *shape, const ds_moe_kv_cache 
                           int64_t q_stride, int32_t max_new) {
   if (check_attn_shape(shape, nullptr, 0) || check_kv_cache(shape, cache, nullptr, 0) || max_new < 0 || q_stride < 0)
     return DS_ERR_INVALID_ARG;
-  return DS_ATTN_GENERIC;
+  return path_of(*shape, *cache, q, q_stride, 2, max_new);
 }
 
 int ds_moe_attention_workspace_bytes(const ds_moe_attn_shape *shape, int32_t n_requests, int64_t T, int32_t max_new,
@@ -136,7 +153,8 @@ int ds_moe_attention_workspace_bytes(const ds_moe_attn_shape *shape, int32_t n_r
   if (!bytes) return fail(err, errlen, DS_ERR_INVALID_ARG, "bytes is NULL");
   if (n_requests < 0 || max_new < 0 || T < 0 || T > (1 << 24))
     return fail(err, errlen, DS_ERR_INVALID_ARG, "n_requests, T or max_new out of range");
-  *bytes = 256;
+  const int64_t rows = (int64_t)max_new * (shape->n_head / shape->n_head_kv);
+  *bytes = (attention_decode_workspace(std::min(rows, AD_MAX_ROWS), launch_blocks()) + 255) / 256 * 256;
   return DS_OK;
 }
 
@@ -173,13 +191,17 @@ int ds_moe_paged_attention(const ds_moe_attn_shape *shape, const ds_moe_kv_cache
   a.cu = cu_new; a.seq = seq_lens; a.T = (int)T; a.R = n_requests; a.max_new = max_new;
   a.out = (uint16_t *)out; a.os = out_stride; a.lse = lse;
   a.H = shape->n_head; a.G = shape->n_head_kv; a.g = a.H / a.G; a.D = shape->head_dim;
-  a.page = shape->page_size; a.window = shape->window;
+  a.page = shape->page_size;
+  a.window = std::min(shape->window, 1 << 30);  // positions stay below 2^30, and sums of two in an int
   const float scale = shape->scale != 0.f ? shape->scale : (float)(1.0 / sqrt((double)a.D));
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  a.max_seq = (int64_t)table_width * a.page;
+  a.max_seq = std::min<int64_t>((int64_t)table_width * a.page, 1 << 30);
   if (!(a.status = status_word())) return fail(err, errlen, DS_ERR_CUDA, "no CUDA device");
   const bool bf16 = shape->dtype == DS_BF16;
-  const cudaError_t e = launch_attention_generic(a, bf16, (cudaStream_t)stream);
+  const cudaStream_t st = (cudaStream_t)stream;
+  const int path = table_width ? path_of(*shape, *cache, q, q_stride, T, max_new) : DS_ATTN_GENERIC;
+  const cudaError_t e = path == DS_ATTN_DECODE ? launch_attention_decode(a, bf16, workspace, st)
+                                               : launch_attention_generic(a, bf16, st);
   return e == cudaSuccess ? DS_OK : cuda_fail(err, errlen, e, "attention");
 }
 

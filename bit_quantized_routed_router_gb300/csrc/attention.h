@@ -24,6 +24,10 @@ struct AttnArgs {
   unsigned *status;
 };
 
+// Query rows a key head up to which the decode kernel serves.
+constexpr int64_t AD_MAX_ROWS = 64;
+size_t attention_decode_workspace(int64_t rows, int blocks);
+cudaError_t launch_attention_decode(const AttnArgs &a, bool bf16, void *ws, cudaStream_t s);
 cudaError_t launch_attention_generic(const AttnArgs &a, bool bf16, cudaStream_t s);
 
 }  // namespace dsm

@@ -1,0 +1,484 @@
+// Attention of few query rows a key head (one new token, or a few drafted
+// ones, with the query heads that share the key head): bound by reading the
+// cache.
+//
+// The keys are the rows of the tensor-core tiles and the queries their
+// columns: S^T = K Q^T is 128 keys x N, O^T += V^T P^T is head_dim x N, with
+// N = 16, 32 or 64, so the work of the softmax and of the matrix products
+// goes with the query rows there are, not with a tile of 128 of them.  A
+// block is
+//
+//   producer warp   copies the tiles' keys and values out of their pages
+//                   (TMA, 128-byte swizzle) into a ring of slots, and the
+//                   query rows;
+//   MMA thread      S^T(f) as soon as tile f's keys are there, O^T(f) when
+//                   its probabilities are;
+//   two groups of four warps, which take the tiles in turn, each with its own
+//                   scores, running maxima and accumulators: one exponentiates
+//                   while the other's products run.  A thread owns one key of
+//                   the tile, and one element of the head in the accumulators.
+//
+// Maxima are raised lazily (AT_SLACK), so that a tile usually costs its group
+// one barrier.  The two groups' sums are joined at the end of a segment.
+#include "attention_tc.cuh"
+
+namespace dsm {
+namespace {
+
+constexpr int AD_THREADS = 320;  // two groups of 128, MMA warp, producer warp
+constexpr int AD_MMA = 8, AD_PRODUCER = 9;
+
+template <int N, int DP>
+struct AdCfg {
+  static constexpr uint32_t TILE = AT_KEYS * DP * 2;
+  static constexpr uint32_t Q = N * DP * 2, P = N * AT_KEYS * 2;
+  static constexpr int ROOM = 227 * 1024 - 1024 - 2 * (Q + P) - 8192;
+  static constexpr int SLOTS = ROOM / (int)TILE < 12 ? ROOM / (int)TILE : 12;
+};
+
+template <int N, int SLOTS>
+struct AdShared {
+  uint64_t full[SLOTS], empty[SLOTS];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  float ref[2][N];      // running maximum of each query row, by group
+  float factor[2][N];   // what a raised maximum multiplies sums with
+  float top[2][4][N];   // a tile's largest score, by warp
+  float sum[2][4][N];   // sums of probabilities, by warp
+  uint32_t odd[2][4];   // keys whose values are not all finite
+  int64_t part[AD_THREADS / 32];
+  Start start;
+  uint32_t tmem;
+  int gave_up;
+};
+
+template <int N, int DP, bool BF16>
+__global__ void __launch_bounds__(AD_THREADS, 1)
+    attention_decode_kernel(const AttnArgs a, const Pieces pieces, const __grid_constant__ CUtensorMap tm_q,
+                            const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, int rows) {
+  using C = AdCfg<N, DP>;
+  constexpr int SLOTS = C::SLOTS, TPB = 1 << 20;  // one block of tokens a request
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint8_t *ring = smem, *qbuf = ring + SLOTS * C::TILE, *pbuf = qbuf + 2 * C::Q;
+  typedef AdShared<N, SLOTS> Sh;
+  Sh &S = *reinterpret_cast<Sh *>(pbuf + 2 * C::P);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  if (tid == 0) {
+    for (int i = 0; i < SLOTS; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.q_full[i], 1);
+      mbar_init(&S.q_empty[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.o_full[i], 1);
+      pieces.what[2 * blockIdx.x + i] = make_int4(0, 0, 0, 0);
+    }
+    mbar_init(&S.drain, 1);
+    S.gave_up = 0;
+    fence_mbar_init();
+  }
+  // query rows that no copy fills stay zero
+  for (int i = tid; i < (int)(2 * C::Q / 16); i += AD_THREADS) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  find_start<AD_THREADS>(a, TPB, &S.start, S.part);
+  __syncthreads();
+  if (S.start.left == 0) return;
+  if (warp == AD_MMA) tmem_alloc<4 * N>(&S.tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;  // scores of the groups at 0 and N, sums at 2 N and 3 N
+  const int F = (int)S.start.left;
+  // places in the ring: K0 K1 V0 K2 V1 ... V(F-1), the order of their use
+  auto k_at = [](int f) { return f ? 2 * f - 1 : 0; };
+  auto v_at = [F](int f) { return f == F - 1 ? 2 * F - 1 : 2 * f + 2; };
+  Segments s;
+  s.init(a, TPB, S.start);
+
+  if (warp == AD_PRODUCER) {
+    // ------------------------------------------------------------ copies --
+    int issued = 0;
+    bool ok = true, bad = false;
+    auto slot_of = [&](int at) -> uint8_t * {
+      const int sl = at % SLOTS;
+      if (at >= SLOTS) {
+        int w = 1;
+        if (lane == 0) w = at_wait(&S.empty[sl], ((at / SLOTS) & 1) ^ 1, &S.gave_up, a.status);
+        if (!__shfl_sync(0xffffffffu, w, 0)) ok = false;
+      }
+      return ring + sl * C::TILE;
+    };
+    int f = 0, segs = 0;
+    TileRuns runs, prev{};
+    int prev_head = 0;
+    while (ok && s.count) {
+      const int b = s.index & 1;
+      if (s.index >= 2) {
+        int w = 1;
+        if (lane == 0) w = at_wait(&S.q_empty[b], ((s.index >> 1) & 1) ^ 1, &S.gave_up, a.status);
+        if (!__shfl_sync(0xffffffffu, w, 0)) break;
+      }
+      if (lane == 0) {
+        const int tokens = N / a.g;
+        mbar_arrive_expect_tx(&S.q_full[b], tokens * a.g * DP * 2);
+#pragma unroll
+        for (int x = 0; x < DP; x += 64)
+          tma_load_3d(qbuf + b * C::Q + x / 64 * (N * 128), &tm_q, x, s.h * a.g, s.sp.t0, &S.q_full[b]);
+      }
+      __syncwarp();
+      ++segs;
+      for (int i = 0; ok && i < s.count; ++i, ++f) {
+        runs.find(a, s, s.tile + i, rows, bad);
+        uint8_t *dst = slot_of(k_at(f));
+        if (!ok) break;
+        runs.copy<DP>(dst, &tm_k, s.h, rows, &S.full[k_at(f) % SLOTS]);
+        issued = k_at(f) + 1;
+        if (f) {
+          dst = slot_of(v_at(f - 1));
+          if (!ok) break;
+          prev.copy<DP>(dst, &tm_v, prev_head, rows, &S.full[v_at(f - 1) % SLOTS]);
+          issued = v_at(f - 1) + 1;
+        }
+        prev = runs;
+        prev_head = s.h;
+      }
+      s.next(a, TPB);
+    }
+    if (ok && f == F) {
+      uint8_t *dst = slot_of(v_at(F - 1));
+      if (ok) {
+        prev.copy<DP>(dst, &tm_v, prev_head, rows, &S.full[v_at(F - 1) % SLOTS]);
+        issued = v_at(F - 1) + 1;
+      }
+    }
+    if (bad) flag(a.status, ST_PAGING);
+    if (lane == 0) {  // every copy has landed before the block ends
+      int off = 0;
+      for (int at = issued > SLOTS ? issued - SLOTS : 0; at < issued; ++at)
+        at_wait(&S.full[at % SLOTS], (at / SLOTS) & 1, &off, a.status);
+      for (int q = segs > 2 ? segs - 2 : 0; q < segs; ++q) at_wait(&S.q_full[q & 1], (q >> 1) & 1, &off, a.status);
+    }
+  } else if (warp == AD_MMA) {
+    // ----------------------------------------------------------- products --
+    if (lane == 0) {
+      const uint32_t idesc = f16_idesc(N, BF16);
+      Segments sk = s;
+      int ik = 0, iv = 0;  // tiles of the segments that scores and sums are at
+      bool ok = true;
+      auto scores = [&](int f) {
+        const int at = k_at(f), sl = at % SLOTS, b = sk.index & 1;
+        if (ik == 0 && !at_wait(&S.q_full[b], (sk.index >> 1) & 1, &S.gave_up, a.status)) ok = false;
+        if (!ok || !at_wait(&S.full[sl], (at / SLOTS) & 1, &S.gave_up, a.status)) { ok = false; return; }
+        tc_fence_after();
+        const uint32_t kb = smem_u32(ring + sl * C::TILE), qb = smem_u32(qbuf + b * C::Q);
+#pragma unroll
+        for (int x = 0; x < DP / 16; ++x)
+          mma_f16(tmem + (f & 1) * N, sw128_desc(kb + x / 4 * (AT_KEYS * 128) + x % 4 * 32),
+                  sw128_desc(qb + x / 4 * (N * 128) + x % 4 * 32), idesc, x > 0);
+        mma_commit(&S.empty[sl]);
+        mma_commit(&S.s_full[f & 1]);
+        if (++ik == sk.count) {
+          mma_commit(&S.q_empty[b]);
+          sk.next(a, TPB);
+          ik = 0;
+        }
+      };
+      scores(0);
+      if (ok && F > 1) scores(1);
+      for (int f = 0; ok && f < F; ++f) {
+        const int at = v_at(f), sl = at % SLOTS;
+        if (!at_wait(&S.p_full[f & 1], (f >> 1) & 1, &S.gave_up, a.status)) break;
+        if (!at_wait(&S.full[sl], (at / SLOTS) & 1, &S.gave_up, a.status)) break;
+        tc_fence_after();
+        const uint32_t vb = smem_u32(ring + sl * C::TILE), pb = smem_u32(pbuf + (f & 1) * C::P);
+        // head_dim 64: rows 64..127 of the product repeat other elements and are not used
+#pragma unroll
+        for (int x = 0; x < AT_KEYS / 16; ++x)
+          mma_f16(tmem + (2 + (f & 1)) * N, sw128_mn_desc(vb + x * 2048, DP == 128 ? AT_KEYS * 128 : 1024),
+                  sw128_desc(pb + x / 4 * (N * 128) + x % 4 * 32), idesc | IDESC_A_MN, true);
+        mma_commit(&S.empty[sl]);
+        if (iv + 2 >= s.count) mma_commit(&S.o_full[f & 1]);  // the group's last tile of the segment
+        if (++iv == s.count) {
+          s.next(a, TPB);
+          iv = 0;
+        }
+        if (f + 2 < F) scores(f + 2);
+      }
+      mma_commit(&S.drain);
+      int off = 0;
+      at_wait(&S.drain, 0, &off, a.status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax --
+    // A wait that runs out ends the waiting, not the walk: every thread still
+    // passes every barrier.
+    const int grp = warp >> 2, key = tid & 127, wq = warp & 3;
+    const uint32_t lanes = (uint32_t)(32 * wq) << 16;
+    const uint32_t t_s = tmem + lanes + grp * N, t_o = tmem + lanes + (2 + grp) * N;
+    uint8_t *pm = pbuf + grp * C::P;
+    const uint32_t p_off = (uint32_t)((key >> 6) * (N * 128) + (key & 7) * 2);
+    const int p_chunk = (key & 63) >> 3;
+    const float sc = a.scale_log2;
+    int f = 0, mine = 0, ends = 0;  // tile of the stretch, tiles of this group, its segments
+    for (; s.count; s.next(a, TPB)) {
+      const int nrows = s.n * a.g, pos0 = s.sp.pos0;
+      float l[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) l[c] = 0.f;
+      {
+        const float z[16] = {};
+#pragma unroll
+        for (int c = 0; c < N; c += 16) tmem_st16(t_o + c, z);
+        tmem_st_wait();
+      }
+      if (key < N) S.ref[grp][key] = AT_NONE;
+      named_bar(1 + grp, 128);
+      int done = 0;
+      const int f_end = f + s.count;
+      for (int i = 0; f < f_end; ++f, ++i) {
+        if ((f & 1) != grp) continue;
+        const int j = (s.tile + i) * AT_KEYS + key;
+        // columns [lo, hi) see this key: those of tokens at j .. j + window - 1
+        const int t_lo = max(0, j - pos0), t_hi = a.window ? min(s.n, j - pos0 + a.window) : s.n;
+        const int lo = min(t_lo, 1 << 16) * a.g, hi = t_hi > t_lo ? t_hi * a.g : 0;
+        const int j0 = (s.tile + i) * AT_KEYS;
+        const bool edge = j0 + AT_KEYS - 1 > pos0 || (a.window && j0 < pos0 + s.n - a.window);
+        at_wait(&S.s_full[grp], mine & 1, &S.gave_up, a.status);
+        tc_fence_after();
+        auto load = [&](int c0, float v[16]) {
+          tmem_ld16(t_s + c0, v);
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[c] = c0 + c >= lo && c0 + c < hi ? v[c] : -INFINITY;
+          }
+        };
+        bool higher = false;
+#pragma unroll
+        for (int c0 = 0; c0 < N; c0 += 16) {
+          float v[16];
+          load(c0, v);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) higher |= v[c] * sc > S.ref[grp][c0 + c] + AT_SLACK;
+        }
+        if (bar_or(1 + grp, 128, higher)) {
+          // raise the maxima to the tile's, and bring sums down to them
+          for (int c0 = 0; c0 < N; c0 += 16) {
+            float v[16];
+            load(c0, v);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float x = isnan(v[c]) ? -INFINITY : v[c] * sc;
+              const uint32_t k = __reduce_max_sync(0xffffffffu, ord_key(x));
+              if (lane == 0) S.top[grp][wq][c0 + c] = ord_val(k);
+            }
+          }
+          named_bar(1 + grp, 128);
+          if (key < N) {
+            const float was = S.ref[grp][key];
+            const float now = fmaxf(fmaxf(fmaxf(S.top[grp][0][key], S.top[grp][1][key]),
+                                          fmaxf(S.top[grp][2][key], S.top[grp][3][key])), was);
+            S.ref[grp][key] = now;
+            S.factor[grp][key] = ex2(was - now);
+          }
+          named_bar(1 + grp, 128);
+#pragma unroll
+          for (int c = 0; c < N; ++c) l[c] *= S.factor[grp][c];
+          if (done) {  // (this group's earlier products are complete: its scores were issued behind them)
+#pragma unroll
+            for (int c0 = 0; c0 < N; c0 += 16) {
+              float o[16];
+              tmem_ld16(t_o + c0, o);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) o[c] *= S.factor[grp][c0 + c];
+              tmem_st16(t_o + c0, o);
+            }
+            tmem_st_wait();
+          }
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < N; c0 += 16) {
+          float v[16];
+          load(c0, v);
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            const float p0 = ex2(fmaf(v[c], sc, -S.ref[grp][c0 + c])), p1 = ex2(fmaf(v[c + 1], sc, -S.ref[grp][c0 + c + 1]));
+            l[c0 + c] += p0;
+            l[c0 + c + 1] += p1;
+            const uint32_t w = pack16<BF16>(p0, p1);
+            uint8_t *at = pm + p_off + (c0 + c) * 128;
+            *reinterpret_cast<uint16_t *>(at + ((p_chunk ^ (c & 7)) << 4)) = (uint16_t)w;
+            *reinterpret_cast<uint16_t *>(at + 128 + ((p_chunk ^ ((c + 1) & 7)) << 4)) = (uint16_t)(w >> 16);
+          }
+        }
+        if (edge) {
+          // values that not every row sees: a probability of zero does not
+          // take away an infinity or NaN, so rows that no token sees are
+          // cleared, and what is not finite in others is added to the sums of
+          // the rows that see it, and cleared
+          const int va = v_at(f);
+          at_wait(&S.full[va % SLOTS], (va / SLOTS) & 1, &S.gave_up, a.status);
+          uint8_t *vt = ring + (va % SLOTS) * C::TILE, *vr = vt + key * 128;
+          bool odd = false;
+          if (hi <= lo) {
+#pragma unroll
+            for (int x = 0; x < DP / 8; ++x)
+              *reinterpret_cast<uint4 *>(vr + x / 8 * (AT_KEYS * 128) + x % 8 * 16) = make_uint4(0, 0, 0, 0);
+          } else if (lo > 0 || hi < nrows) {
+#pragma unroll
+            for (int x = 0; x < DP / 8; ++x) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(vr + x / 8 * (AT_KEYS * 128) + x % 8 * 16);
+              odd |= not_finite2<BF16>(w.x) || not_finite2<BF16>(w.y) || not_finite2<BF16>(w.z) || not_finite2<BF16>(w.w);
+            }
+          }
+          if (s.n > 1 && bar_or(1 + grp, 128, odd)) {
+            const uint32_t m = __ballot_sync(0xffffffffu, odd);
+            if (lane == 0) S.odd[grp][wq] = m;
+            named_bar(1 + grp, 128);
+            const int d = key & (DP - 1);
+            for (int k = 0; k < AT_KEYS; ++k) {
+              if (!(S.odd[grp][k >> 5] >> (k & 31) & 1u)) continue;
+              const uint16_t x = *reinterpret_cast<const uint16_t *>(vt + d / 64 * (AT_KEYS * 128) + k * 128 +
+                                                                     ((((d & 63) >> 3) ^ (k & 7)) << 4) + (d & 7) * 2);
+              const float add = not_finite2<BF16>(x) ? (BF16 ? bf16_to_f32(x) : fp16_to_f32(x)) : 0.f;
+              const int jk = j0 + k, k_lo = max(0, jk - pos0), k_hi = a.window ? min(s.n, jk - pos0 + a.window) : s.n;
+              for (int c0 = 0; c0 < N; c0 += 16) {
+                float o[16];
+                tmem_ld16(t_o + c0, o);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  if (c0 + c >= k_lo * a.g && c0 + c < k_hi * a.g) o[c] += add;
+                tmem_st16(t_o + c0, o);
+              }
+              tmem_st_wait();
+            }
+            named_bar(1 + grp, 128);
+            if (odd) {
+              for (int x = 0; x < DP / 2; ++x) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(vr + x / 32 * (AT_KEYS * 128) + x % 32 * 4);
+                if (not_finite2<BF16>(*w & 0xFFFFu)) *w &= 0xFFFF0000u;
+                if (not_finite2<BF16>(*w & 0xFFFF0000u)) *w &= 0xFFFFu;
+              }
+            }
+          }
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[grp]);
+        ++mine;
+        ++done;
+      }
+      // ---- the segment's end: each group finishes half of the rows ----
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        const float t = warp_sum(l[c]);
+        if (lane == 0) S.sum[grp][wq][c] = t;
+      }
+      if (done) {
+        at_wait(&S.o_full[grp], ends & 1, &S.gave_up, a.status);
+        ++ends;
+        tc_fence_after();
+      }
+      // both groups' products are done before the probabilities' room is
+      // taken for the exchange: [rows][DP] sums
+      named_bar(3, 256);
+      float *ex = reinterpret_cast<float *>(pbuf);
+      constexpr int HALF = N / 2;
+      float o[HALF];
+#pragma unroll
+      for (int c = 0; c < HALF; c += 8) tmem_ld8(t_o + (1 - grp) * HALF + c, o + c);
+      if (key < DP) {
+#pragma unroll
+        for (int c = 0; c < HALF; ++c) ex[((1 - grp) * HALF + c) * DP + key] = o[c];
+      }
+#pragma unroll
+      for (int c = 0; c < HALF; c += 8) tmem_ld8(t_o + grp * HALF + c, o + c);
+      tc_fence_before();
+      named_bar(3, 256);
+      const bool whole = s.has_start() && s.has_end();
+      const int64_t piece = 2 * (int64_t)blockIdx.x + (s.index > 0);
+#pragma unroll
+      for (int c = 0; c < HALF; ++c) {
+        const int row = grp * HALF + c;
+        if (row >= nrows) continue;
+        const float m0 = S.ref[0][row], m1 = S.ref[1][row], m = fmaxf(m0, m1), w0 = ex2(m0 - m), w1 = ex2(m1 - m);
+        const float s0 = (S.sum[0][0][row] + S.sum[0][1][row]) + (S.sum[0][2][row] + S.sum[0][3][row]);
+        const float s1 = (S.sum[1][0][row] + S.sum[1][1][row]) + (S.sum[1][2][row] + S.sum[1][3][row]);
+        const float total = s0 * w0 + s1 * w1;
+        const float own = o[c];
+        if (whole) {
+          const int64_t t = s.sp.t0 + row / a.g;
+          const int h = s.h * a.g + row % a.g;
+          if (key < a.D) {
+            const float v = own * (grp ? w1 : w0) + ex[row * DP + key] * (grp ? w0 : w1);
+            a.out[t * a.os + (int64_t)h * a.D + key] = (uint16_t)pack16<BF16>(total == 0.f ? 0.f : v / total, 0.f);
+          }
+          if (a.lse && key == 0) a.lse[t * a.H + h] = total == 0.f ? -INFINITY : (m + log2f(total)) * AT_LN2;
+        } else {
+          if (key < DP) pieces.sums[(piece * N + row) * DP + key] = own * (grp ? w1 : w0) + ex[row * DP + key] * (grp ? w0 : w1);
+          if (key == 0) pieces.stats[piece * N + row] = make_float2(m, total);
+        }
+      }
+      if (!whole && tid == 0)
+        pieces.what[piece] = make_int4(s.r, s.h, 0, PIECE_USED | (s.has_start() ? PIECE_START : 0) | (s.has_end() ? PIECE_END : 0));
+      named_bar(3, 256);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == AD_MMA) {
+    tc_fence_after();
+    tmem_free<4 * N>(tmem);
+  }
+}
+
+template <int N, int DP, bool BF16>
+cudaError_t launch(const AttnArgs &a, void *ws, cudaStream_t s) {
+  using C = AdCfg<N, DP>;
+  constexpr size_t smem = 1024 + C::SLOTS * C::TILE + 2 * (C::Q + C::P) + sizeof(AdShared<N, C::SLOTS>);
+  static_assert(smem <= 227 * 1024, "shared memory of a block");
+  static OncePerDevice once;
+  cudaError_t e = once_per_device(once, []() {
+    return cudaFuncSetAttribute(attention_decode_kernel<N, DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (e != cudaSuccess) return e;
+  const int blocks = device_sms(), rows = piece_rows(a.page);
+  CUtensorMap tq, tk, tv;
+  if (!make_q_map(&tq, a, N / a.g, BF16) || !make_kv_map(&tk, a.k, a, rows, BF16) || !make_kv_map(&tv, a.v, a, rows, BF16))
+    return cudaErrorInvalidValue;
+  const Pieces p = pieces_of(ws, blocks, N, DP);
+  attention_decode_kernel<N, DP, BF16><<<blocks, AD_THREADS, smem, s>>>(a, p, tq, tk, tv, rows);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks, N / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, BF16>, a, p, N, 1 << 20);
+}
+
+template <int N>
+cudaError_t launch_n(const AttnArgs &a, bool bf16, void *ws, cudaStream_t s) {
+  if (a.D <= 64) return bf16 ? launch<N, 64, true>(a, ws, s) : launch<N, 64, false>(a, ws, s);
+  return bf16 ? launch<N, 128, true>(a, ws, s) : launch<N, 128, false>(a, ws, s);
+}
+
+int columns(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+}  // namespace
+
+size_t attention_decode_workspace(int64_t rows, int blocks) { return pieces_bytes(blocks, columns(rows), 128); }
+
+cudaError_t launch_attention_decode(const AttnArgs &a, bool bf16, void *ws, cudaStream_t s) {
+  const int n = columns((int64_t)a.max_new * a.g);
+  return n == 16 ? launch_n<16>(a, bf16, ws, s) : n == 32 ? launch_n<32>(a, bf16, ws, s) : launch_n<64>(a, bf16, ws, s);
+}
+
+}  // namespace dsm

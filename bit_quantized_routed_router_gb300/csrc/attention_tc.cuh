@@ -1,0 +1,378 @@
+// What the tensor-core attention kernels share: how a launch's work is split,
+// the copies of keys and values out of their pages, and the joining of
+// pieces.
+//
+// Work is counted in tiles of 128 keys.  An item is a block of query rows
+// (tpb tokens of one request, with the query heads that share a key head)
+// and the tiles that any of its tokens sees; items follow one another by
+// request, key head and block.  The tiles of all items form one line, which
+// the launch's blocks share out evenly whatever the lengths are: a block
+// takes a stretch of the line, so it begins inside an item and ends inside
+// another.  Each such piece leaves its sums, unnormalised, in the workspace
+// (at most two a block), and a second kernel joins them in the order of the
+// keys, so results do not depend on timing.
+#pragma once
+#include <float.h>
+
+#include "attention.h"
+#include "common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "serving.cuh"
+#include "tcgen05.cuh"
+
+namespace dsm {
+namespace {
+
+constexpr int AT_KEYS = 128;
+constexpr uint64_t AT_LIMIT_NS = 2000000000ull;
+constexpr float AT_LN2 = 0.69314718055994531f;
+// A running maximum is raised only when a score exceeds it by this much (in
+// powers of two): probabilities then stay below 2^8, which costs nothing in a
+// 16-bit float, and accumulators are rarely rescaled.
+constexpr float AT_SLACK = 8.f;
+constexpr float AT_NONE = -FLT_MAX;  // maximum of no scores
+
+// Bounded wait; once one has run out, every wait gives up at once.
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t par, int *gave_up, unsigned *status) {
+  if (mbar_try_wait(bar, par)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_sleep(bar, par, 2000u)) {
+    if (*(volatile int *)gave_up) return false;
+    if (globaltimer_ns() - t0 > AT_LIMIT_NS) {
+      flag(status, ST_TIMEOUT);
+      *(volatile int *)gave_up = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// Whether any of the `count` threads at named barrier `id` says so.
+__device__ __forceinline__ bool bar_or(int id, int count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two floats as 16-bit ones, a in the low half.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Whether either 16-bit float of a word is an infinity or NaN.
+template <bool BF16>
+__device__ __forceinline__ bool not_finite2(uint32_t w) {
+  constexpr uint32_t M = BF16 ? 0x7F80u : 0x7C00u;
+  return (w & M) == M || (w & (M << 16)) == (M << 16);
+}
+
+// Tiles [begin, end) that tokens first .. first + n - 1 of a request see: one
+// at least, so that a block of tokens that sees no key is still written.
+__device__ __forceinline__ void tile_range(const Span &s, int first, int n, int window, int &begin, int &end) {
+  const int p = s.pos0 + first, lo = window && p + 1 > window ? p + 1 - window : 0;
+  begin = lo / AT_KEYS;
+  end = max(begin + 1, (p + n + AT_KEYS - 1) / AT_KEYS);
+}
+
+__device__ __forceinline__ int64_t request_tiles(const Span &s, int tpb, int window) {
+  int64_t sum = 0;
+  for (int f = 0; f < s.n; f += tpb) {
+    int b, e;
+    tile_range(s, f, min(tpb, s.n - f), window, b, e);
+    sum += e - b;
+  }
+  return sum;
+}
+
+// Where a block's stretch begins, and how many tiles it has.
+struct Start {
+  int r, h, b, tile;
+  int64_t left;
+};
+
+// By all THREADS threads; *out is in shared memory and valid after the
+// caller's next barrier.
+template <int THREADS>
+__device__ __forceinline__ void find_start(const AttnArgs &a, int tpb, Start *out, int64_t *part) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.R + THREADS - 1) / THREADS, r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
+  bool bad = false;
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r)
+    mine += request_tiles(request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad), tpb, a.window);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  total *= a.G;
+  before *= a.G;
+  // with fewer tiles than blocks the first blocks have one each
+  const int64_t c = blockIdx.x, blocks = gridDim.x;
+  const int64_t s = total >= blocks ? total * c / blocks : min(c, total);
+  const int64_t e = total >= blocks ? total * (c + 1) / blocks : min(c + 1, total);
+  if (tid == 0) out->left = e - s;
+  if (s >= before && s < before + mine * a.G) {
+    int64_t off = s - before;
+    for (int r = r0; r < r1; ++r) {
+      const Span sp = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
+      const int64_t tr = request_tiles(sp, tpb, a.window);
+      if (off >= tr * a.G) {
+        off -= tr * a.G;
+        continue;
+      }
+      out->r = r;
+      out->h = (int)(off / tr);
+      off %= tr;
+      int b = 0, t0, t1;
+      for (;; ++b) {
+        tile_range(sp, b * tpb, min(tpb, sp.n - b * tpb), a.window, t0, t1);
+        if (off < t1 - t0) break;
+        off -= t1 - t0;
+      }
+      out->b = b;
+      out->tile = t0 + (int)off;
+      break;
+    }
+  }
+  if (bad && blockIdx.x == 0) flag(a.status, ST_PAGING);
+}
+
+// The segments of a block's stretch, in order: runs of tiles of one item.
+struct Segments {
+  int r, h, b, tile, begin, end, count, index;
+  int64_t left;
+  Span sp;
+  // of the segment: its first token in the request, its tokens
+  int first, n;
+
+  __device__ __forceinline__ void init(const AttnArgs &a, int tpb, const Start &s) {
+    r = s.r; h = s.h; b = s.b; left = s.left;
+    index = 0;
+    if (left > 0) {
+      bool bad = false;
+      sp = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
+      item(a, tpb);
+      tile = s.tile;
+    }
+    size();
+  }
+  __device__ __forceinline__ void item(const AttnArgs &a, int tpb) {
+    first = b * tpb;
+    n = min(tpb, sp.n - first);
+    tile_range(sp, first, n, a.window, begin, end);
+    tile = begin;
+  }
+  __device__ __forceinline__ void size() { count = left > 0 ? (int)min(left, (int64_t)(end - tile)) : 0; }
+  __device__ __forceinline__ bool has_start() const { return tile == begin; }
+  __device__ __forceinline__ bool has_end() const { return tile + count == end; }
+  __device__ __forceinline__ void next(const AttnArgs &a, int tpb) {
+    left -= count;
+    ++index;
+    if (left > 0) {
+      if (++b * tpb >= sp.n) {
+        b = 0;
+        if (++h == a.G) {
+          h = 0;
+          bool bad = false;
+          do {
+            if (++r >= a.R) {  // lengths that changed under the kernel
+              left = 0;
+              break;
+            }
+            sp = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
+          } while (sp.n == 0);
+        }
+      }
+      if (left > 0) item(a, tpb);
+    }
+    size();
+  }
+};
+
+// Pieces: two a block, described by (r, h, b, flags), with `rows` rows of DP
+// sums, and each row's maximum and sum of probabilities.
+constexpr int PIECE_USED = 1, PIECE_START = 2, PIECE_END = 4;
+struct Pieces {
+  int4 *what;     // [2 blocks]
+  float *sums;    // [2 blocks][rows][DP]
+  float2 *stats;  // [2 blocks][rows]: maximum, sum
+};
+__host__ __device__ inline size_t pieces_bytes(int blocks, int rows, int dp) {
+  const size_t n = 2 * (size_t)blocks;
+  return (n * 16 + 255) / 256 * 256 + n * rows * (dp * 4 + 8);
+}
+inline Pieces pieces_of(void *ws, int blocks, int rows, int dp) {
+  const size_t n = 2 * (size_t)blocks;
+  Pieces p;
+  p.what = (int4 *)ws;
+  p.sums = (float *)((char *)ws + (n * 16 + 255) / 256 * 256);
+  p.stats = (float2 *)(p.sums + n * rows * dp);
+  return p;
+}
+
+// One warp a row: the pieces of an item that several blocks share, joined in
+// the order of its keys.  Block x looks at the piece that block x of the
+// attention began and did not end.
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a, const Pieces p, int rows, int tpb) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int PER = DP / 32;
+  int at = 2 * blockIdx.x + 1;
+  int4 w = p.what[at];
+  if ((w.w & (PIECE_USED | PIECE_START | PIECE_END)) != (PIECE_USED | PIECE_START)) {
+    w = p.what[--at];
+    if ((w.w & (PIECE_USED | PIECE_START | PIECE_END)) != (PIECE_USED | PIECE_START)) return;
+  }
+  bool bad = false;
+  const Span sp = request_span(a.cu, a.seq, w.x, a.T, a.max_new, a.max_seq, bad);
+  const int first = w.z * tpb, row = blockIdx.y * 4 + warp;
+  if (row >= min(tpb, sp.n - first) * a.g) return;
+  // how many pieces: up to the block whose first piece ends the item
+  int n = 1;
+  for (int c = blockIdx.x + 1;; c += 32) {
+    const int e = c + lane < gridDim.x ? p.what[2 * (c + lane)].w : PIECE_END;
+    const unsigned ends = __ballot_sync(0xffffffffu, e & PIECE_END);
+    n += ends ? __ffs(ends) : 32;
+    if (ends) break;
+  }
+  n = min(n, (int)(gridDim.x - blockIdx.x));
+  auto piece = [&](int i) { return (int64_t)(i ? 2 * (blockIdx.x + i) : at) * rows + row; };
+  float m = AT_NONE;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.stats[piece(i)].x);
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+  float l = 0.f, o[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) o[i] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float2 st = make_float2(AT_NONE, 0.f);
+    if (i0 + lane < n) st = p.stats[piece(i0 + lane)];
+    const float w = ex2(st.x - m), lw = st.y * w;
+    const int k = min(32, n - i0);
+#pragma unroll 8
+    for (int i = 0; i < k; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      l += __shfl_sync(0xffffffffu, lw, i);
+      const float *src = p.sums + piece(i0 + i) * DP + PER * lane;
+#pragma unroll
+      for (int x = 0; x < PER; x += 2) {
+        const float2 f = *reinterpret_cast<const float2 *>(src + x);
+        o[x] = fmaf(f.x, wi, o[x]);
+        o[x + 1] = fmaf(f.y, wi, o[x + 1]);
+      }
+    }
+  }
+  const int64_t t = sp.t0 + first + row / a.g;
+  const int h = w.y * a.g + row % a.g;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t *out = a.out + t * a.os + (int64_t)h * a.D + PER * lane;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (PER * lane + i < a.D) out[i] = (uint16_t)pack16<BF16>(o[i] * inv, 0.f);
+  if (a.lse && lane == 0) a.lse[t * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * AT_LN2;
+}
+
+// The keys or values as a 4-D map {element, row of a page, head, page} with
+// boxes of 64 elements x `rows` rows.  A box that begins at page -1 is
+// outside the map: the copy fills it with zeros and reads nothing.
+inline bool make_kv_map(CUtensorMap *m, const void *base, const AttnArgs &a, int rows, bool bf16) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  auto stride = [](int64_t n, int64_t s) { return n > 1 ? (cuuint64_t)s * 2 : (cuuint64_t)16; };
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.page, (cuuint64_t)a.G, (cuuint64_t)a.n_pages};
+  const cuuint64_t strides[3] = {stride(a.page, a.rs), stride(a.G, a.hs), stride(a.n_pages, a.ps)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The query rows {element, head, token}: a box is 64 elements of the g heads
+// of `tokens` tokens, so that row t * g + i of a tile is head i of token t.
+inline bool make_q_map(CUtensorMap *m, const AttnArgs &a, int tokens, bool bf16) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.H, (cuuint64_t)a.T};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, a.T > 1 ? (cuuint64_t)a.qs * 2 : (cuuint64_t)a.D * a.H * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)a.g, (cuuint32_t)tokens}, estr[3] = {1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t *>(a.q),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows that one copy can take: the largest power of two that divides a page,
+// so that a copy never runs over a page's end; at most a tile.
+inline int piece_rows(int page) {
+  int b = 1;
+  while (b < AT_KEYS && page % (2 * b) == 0) b *= 2;
+  return b;
+}
+
+// The copies of one tile's keys (and later its values): lane i < 128 / rows
+// has the i-th run of rows, its page and its first row there.  Runs that no
+// token of the segment sees, and pages that are none, are filled with zeros.
+struct TileRuns {
+  int page, row;
+  __device__ __forceinline__ void find(const AttnArgs &a, const Segments &s, int tile, int rows, bool &bad) {
+    const int lane = threadIdx.x & 31, j = tile * AT_KEYS + lane * rows;
+    page = -1;
+    row = 0;
+    const int p = s.sp.pos0 + s.first, lo = a.window ? p + 1 - a.window : 0;
+    if (lane * rows < AT_KEYS && j < p + s.n && j + rows > lo) {
+      const int col = j / a.page;
+      row = j - col * a.page;
+      page = a.table[s.r * a.table_stride + col];
+      if (page < 0 || page >= a.n_pages) {
+        page = -1;
+        row = 0;
+        bad = true;
+      }
+    }
+  }
+  template <int DP>
+  __device__ __forceinline__ void copy(uint8_t *slot, const CUtensorMap *map, int head, int rows, uint64_t *full) const {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) mbar_arrive_expect_tx(full, AT_KEYS * DP * 2);
+    __syncwarp();
+    if (lane * rows < AT_KEYS) {
+#pragma unroll
+      for (int x = 0; x < DP; x += 64)
+        tma_load_4d(slot + x / 64 * (AT_KEYS * 128) + lane * rows * 128, map, x, row, head, page, full);
+    }
+    __syncwarp();
+  }
+};
+
+}  // namespace
+}  // namespace dsm
