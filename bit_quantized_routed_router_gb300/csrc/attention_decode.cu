@@ -8,11 +8,11 @@
 // goes with the query rows there are, not with a tile of 128 of them.  A
 // block is
 //
-//   producer warp   copies the tiles' keys and values out of their pages
-//                   (TMA, 128-byte swizzle) into a ring of slots, and the
-//                   query rows;
-//   MMA thread      S^T(f) as soon as tile f's keys are there, O^T(f) when
-//                   its probabilities are;
+//   two producer warps  copy the tiles' keys (and the query rows), and the
+//                   values, out of their pages (TMA, 128-byte swizzle) into a
+//                   ring of slots each;
+//   MMA thread      S^T of the next four tiles ahead, O^T of a tile when its
+//                   probabilities are there;
 //   two groups of four warps, which take the tiles in turn, each with its own
 //                   scores, running maxima and accumulators: one exponentiates
 //                   while the other's products run.  A thread owns one key of
@@ -25,23 +25,27 @@
 namespace dsm {
 namespace {
 
-constexpr int AD_THREADS = 320;  // two groups of 128, MMA warp, producer warp
-constexpr int AD_MMA = 8, AD_PRODUCER = 9;
+constexpr int AD_THREADS = 352;  // two groups of 128, MMA warp, two producer warps
+constexpr int AD_MMA = 8, AD_KEYS = 9, AD_VALUES = 10;
+constexpr int AD_AHEAD = 4;  // tiles whose scores are computed ahead: two buffers of scores a group
 
 template <int N, int DP>
 struct AdCfg {
   static constexpr uint32_t TILE = AT_KEYS * DP * 2;
   static constexpr uint32_t Q = N * DP * 2, P = N * AT_KEYS * 2;
+  static constexpr int TMEM = N == 64 ? 512 : 8 * N;  // columns: four tiles' scores, two groups' sums
   static constexpr int ROOM = 227 * 1024 - 1024 - 2 * (Q + P) - 8192;
-  static constexpr int SLOTS = ROOM / (int)TILE < 12 ? ROOM / (int)TILE : 12;
+  static constexpr int SLOTS = ROOM / (2 * (int)TILE) < 6 ? ROOM / (2 * (int)TILE) : 6;  // of keys, and of values
 };
 
 template <int N, int SLOTS>
 struct AdShared {
-  uint64_t full[SLOTS], empty[SLOTS];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
-  float ref[2][N];      // running maximum of each query row, by group
-  float factor[2][N];   // what a raised maximum multiplies sums with
+  uint64_t full[2][SLOTS], empty[2][SLOTS];  // keys, values
+  uint64_t q_full[2], q_empty[2], s_full[AD_AHEAD], p_full[2], o_full[2], drain;
+  alignas(16) float ref[2][N];     // running maximum of each query row, by group
+  alignas(16) float factor[2][N];  // what a raised maximum multiplies sums with
+  alignas(16) float2 weight[N];    // of a segment's row: of its finishing group's sums, and of the other's
+  int64_t place[N];                // where the row goes
   float top[2][4][N];   // a tile's largest score, by warp
   float sum[2][4][N];   // sums of probabilities, by warp
   uint32_t odd[2][4];   // keys whose values are not all finite
@@ -59,22 +63,25 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
   constexpr int SLOTS = C::SLOTS, TPB = 1 << 20;  // one block of tokens a request
   extern __shared__ uint8_t raw[];
   uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  uint8_t *ring = smem, *qbuf = ring + SLOTS * C::TILE, *pbuf = qbuf + 2 * C::Q;
+  uint8_t *kring = smem, *vring = kring + SLOTS * C::TILE, *qbuf = vring + SLOTS * C::TILE, *pbuf = qbuf + 2 * C::Q;
   typedef AdShared<N, SLOTS> Sh;
   Sh &S = *reinterpret_cast<Sh *>(pbuf + 2 * C::P);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;");
 
   if (tid == 0) {
-    for (int i = 0; i < SLOTS; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], 1);
+    for (int i = 0; i < 2 * SLOTS; ++i) {
+      mbar_init(&S.full[i / SLOTS][i % SLOTS], 1);
+      mbar_init(&S.empty[i / SLOTS][i % SLOTS], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.q_full[i], 1);
       mbar_init(&S.q_empty[i], 1);
-      mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_full[i], 4);
       mbar_init(&S.o_full[i], 1);
       pieces.what[2 * blockIdx.x + i] = make_int4(0, 0, 0, 0);
     }
+    for (int i = 0; i < AD_AHEAD; ++i) mbar_init(&S.s_full[i], 1);
     mbar_init(&S.drain, 1);
     S.gave_up = 0;
     fence_mbar_init();
@@ -84,127 +91,103 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
   fence_proxy_async();
   find_start<AD_THREADS>(a, TPB, &S.start, S.part);
   __syncthreads();
-  if (S.start.left == 0) return;
-  if (warp == AD_MMA) tmem_alloc<4 * N>(&S.tmem);
+  if (warp == AD_MMA) tmem_alloc<C::TMEM>(&S.tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = S.tmem;  // scores of the groups at 0 and N, sums at 2 N and 3 N
-  const int F = (int)S.start.left;
-  // places in the ring: K0 K1 V0 K2 V1 ... V(F-1), the order of their use
-  auto k_at = [](int f) { return f ? 2 * f - 1 : 0; };
-  auto v_at = [F](int f) { return f == F - 1 ? 2 * F - 1 : 2 * f + 2; };
+  const uint32_t tmem = S.tmem;  // scores of tile f at (f mod 4) N, sums of group i at (4 + i) N
   Segments s;
   s.init(a, TPB, S.start);
-
-  if (warp == AD_PRODUCER) {
+  if (warp == AD_KEYS || warp == AD_VALUES) {
     // ------------------------------------------------------------ copies --
-    int issued = 0;
+    const bool keys = warp == AD_KEYS;
+    const CUtensorMap *map = keys ? &tm_k : &tm_v;
     bool ok = true, bad = false;
-    auto slot_of = [&](int at) -> uint8_t * {
-      const int sl = at % SLOTS;
-      if (at >= SLOTS) {
-        int w = 1;
-        if (lane == 0) w = at_wait(&S.empty[sl], ((at / SLOTS) & 1) ^ 1, &S.gave_up, a.status);
-        if (!__shfl_sync(0xffffffffu, w, 0)) ok = false;
-      }
-      return ring + sl * C::TILE;
-    };
-    int f = 0, segs = 0;
-    TileRuns runs, prev{};
-    int prev_head = 0;
-    while (ok && s.count) {
-      const int b = s.index & 1;
-      if (s.index >= 2) {
-        int w = 1;
-        if (lane == 0) w = at_wait(&S.q_empty[b], ((s.index >> 1) & 1) ^ 1, &S.gave_up, a.status);
-        if (!__shfl_sync(0xffffffffu, w, 0)) break;
-      }
-      if (lane == 0) {
-        const int tokens = N / a.g;
-        mbar_arrive_expect_tx(&S.q_full[b], tokens * a.g * DP * 2);
+    int segs = 0, f = 0, i = 0;  // segments begun, tile of the stretch, of the segment
+    TileRuns now, later;
+    int head = s.h;
+    if (s.count) now.find(a, s, s.tile, rows);
+    for (; s.count; ++f) {
+      if (i == 0) {
+        head = s.h;
+        if (keys) {
+          const int b = s.index & 1;
+          if (lane == 0 && s.index >= 2 && !at_wait(&S.q_empty[b], ((s.index >> 1) & 1) ^ 1, &S.gave_up, a.status)) ok = false;
+          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+          if (lane == 0) {
+            const int tokens = N / a.g;
+            mbar_arrive_expect_tx(&S.q_full[b], tokens * a.g * DP * 2);
 #pragma unroll
-        for (int x = 0; x < DP; x += 64)
-          tma_load_3d(qbuf + b * C::Q + x / 64 * (N * 128), &tm_q, x, s.h * a.g, s.sp.t0, &S.q_full[b]);
-      }
-      __syncwarp();
-      ++segs;
-      for (int i = 0; ok && i < s.count; ++i, ++f) {
-        runs.find(a, s, s.tile + i, rows, bad);
-        uint8_t *dst = slot_of(k_at(f));
-        if (!ok) break;
-        runs.copy<DP>(dst, &tm_k, s.h, rows, &S.full[k_at(f) % SLOTS]);
-        issued = k_at(f) + 1;
-        if (f) {
-          dst = slot_of(v_at(f - 1));
-          if (!ok) break;
-          prev.copy<DP>(dst, &tm_v, prev_head, rows, &S.full[v_at(f - 1) % SLOTS]);
-          issued = v_at(f - 1) + 1;
+            for (int x = 0; x < DP; x += 64)
+              tma_load_3d(qbuf + b * C::Q + x / 64 * (N * 128), &tm_q, x, s.h * a.g, s.sp.t0, &S.q_full[b]);
+          }
+          __syncwarp();
+          ++segs;
         }
-        prev = runs;
-        prev_head = s.h;
       }
-      s.next(a, TPB);
-    }
-    if (ok && f == F) {
-      uint8_t *dst = slot_of(v_at(F - 1));
-      if (ok) {
-        prev.copy<DP>(dst, &tm_v, prev_head, rows, &S.full[v_at(F - 1) % SLOTS]);
-        issued = v_at(F - 1) + 1;
+      if (++i == s.count) {
+        s.next(a, TPB);
+        i = 0;
       }
+      if (s.count) later.find(a, s, s.tile + i, rows);
+      const int sl = f % SLOTS;
+      if (lane == 0 && f >= SLOTS && !at_wait(&S.empty[!keys][sl], ((f / SLOTS) & 1) ^ 1, &S.gave_up, a.status)) ok = false;
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      now.copy<DP>(a, (keys ? kring : vring) + sl * C::TILE, map, head, rows, &S.full[!keys][sl], bad);
+      now = later;
     }
     if (bad) flag(a.status, ST_PAGING);
-    if (lane == 0) {  // every copy has landed before the block ends
+    if (lane == 0) {  // every copy of this warp has landed before the block ends
       int off = 0;
-      for (int at = issued > SLOTS ? issued - SLOTS : 0; at < issued; ++at)
-        at_wait(&S.full[at % SLOTS], (at / SLOTS) & 1, &off, a.status);
-      for (int q = segs > 2 ? segs - 2 : 0; q < segs; ++q) at_wait(&S.q_full[q & 1], (q >> 1) & 1, &off, a.status);
+      for (int g = max(0, f - SLOTS); g < f; ++g) at_wait(&S.full[!keys][g % SLOTS], (g / SLOTS) & 1, &off, a.status);
+      for (int q = max(0, segs - 2); q < segs; ++q) at_wait(&S.q_full[q & 1], (q >> 1) & 1, &off, a.status);
     }
   } else if (warp == AD_MMA) {
     // ----------------------------------------------------------- products --
     if (lane == 0) {
       const uint32_t idesc = f16_idesc(N, BF16);
       Segments sk = s;
-      int ik = 0, iv = 0;  // tiles of the segments that scores and sums are at
+      int ik = 0;  // tile of the segment that scores are at
       bool ok = true;
       auto scores = [&](int f) {
-        const int at = k_at(f), sl = at % SLOTS, b = sk.index & 1;
+        const int sl = f % SLOTS, b = sk.index & 1;
         if (ik == 0 && !at_wait(&S.q_full[b], (sk.index >> 1) & 1, &S.gave_up, a.status)) ok = false;
-        if (!ok || !at_wait(&S.full[sl], (at / SLOTS) & 1, &S.gave_up, a.status)) { ok = false; return; }
+        if (!ok || !at_wait(&S.full[0][sl], (f / SLOTS) & 1, &S.gave_up, a.status)) { ok = false; return; }
         tc_fence_after();
-        const uint32_t kb = smem_u32(ring + sl * C::TILE), qb = smem_u32(qbuf + b * C::Q);
+        const uint64_t kd = sw128_desc(smem_u32(kring + sl * C::TILE)), qd = sw128_desc(smem_u32(qbuf + b * C::Q));
+        const uint32_t d = tmem + (f % AD_AHEAD) * N;
 #pragma unroll
-        for (int x = 0; x < DP / 16; ++x)
-          mma_f16(tmem + (f & 1) * N, sw128_desc(kb + x / 4 * (AT_KEYS * 128) + x % 4 * 32),
-                  sw128_desc(qb + x / 4 * (N * 128) + x % 4 * 32), idesc, x > 0);
-        mma_commit(&S.empty[sl]);
-        mma_commit(&S.s_full[f & 1]);
+        for (int x = 0; x < DP / 16; ++x)  // (addresses in a descriptor count 16 bytes)
+          mma_f16(d, kd + (x / 4 * (AT_KEYS * 128) + x % 4 * 32) / 16, qd + (x / 4 * (N * 128) + x % 4 * 32) / 16, idesc, x > 0);
+        mma_commit(&S.empty[0][sl]);
+        mma_commit(&S.s_full[f % AD_AHEAD]);
         if (++ik == sk.count) {
           mma_commit(&S.q_empty[b]);
           sk.next(a, TPB);
           ik = 0;
         }
       };
-      scores(0);
-      if (ok && F > 1) scores(1);
-      for (int f = 0; ok && f < F; ++f) {
-        const int at = v_at(f), sl = at % SLOTS;
+      for (int f = 0; ok && f < AD_AHEAD && sk.count; ++f) scores(f);
+      int iv = 0;
+      for (int f = 0; ok && s.count; ++f) {
+        const int sl = f % SLOTS;
         if (!at_wait(&S.p_full[f & 1], (f >> 1) & 1, &S.gave_up, a.status)) break;
-        if (!at_wait(&S.full[sl], (at / SLOTS) & 1, &S.gave_up, a.status)) break;
+        if (!at_wait(&S.full[1][sl], (f / SLOTS) & 1, &S.gave_up, a.status)) break;
         tc_fence_after();
-        const uint32_t vb = smem_u32(ring + sl * C::TILE), pb = smem_u32(pbuf + (f & 1) * C::P);
         // head_dim 64: rows 64..127 of the product repeat other elements and are not used
+        const uint64_t vd = sw128_mn_desc(smem_u32(vring + sl * C::TILE), DP == 128 ? AT_KEYS * 128 : 1024);
+        const uint64_t pd = sw128_desc(smem_u32(pbuf + (f & 1) * C::P));
+        const uint32_t d = tmem + (AD_AHEAD + (f & 1)) * N;
 #pragma unroll
         for (int x = 0; x < AT_KEYS / 16; ++x)
-          mma_f16(tmem + (2 + (f & 1)) * N, sw128_mn_desc(vb + x * 2048, DP == 128 ? AT_KEYS * 128 : 1024),
-                  sw128_desc(pb + x / 4 * (N * 128) + x % 4 * 32), idesc | IDESC_A_MN, true);
-        mma_commit(&S.empty[sl]);
-        if (iv + 2 >= s.count) mma_commit(&S.o_full[f & 1]);  // the group's last tile of the segment
+          mma_f16(d, vd + x * 2048 / 16, pd + (x / 4 * (N * 128) + x % 4 * 32) / 16, idesc | IDESC_A_MN, true);
+        mma_commit(&S.empty[1][sl]);
+        mma_commit(&S.o_full[f & 1]);
+        if (sk.count) scores(f + AD_AHEAD);
         if (++iv == s.count) {
           s.next(a, TPB);
           iv = 0;
         }
-        if (f + 2 < F) scores(f + 2);
       }
       mma_commit(&S.drain);
       int off = 0;
@@ -217,12 +200,13 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
     // passes every barrier.
     const int grp = warp >> 2, key = tid & 127, wq = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * wq) << 16;
-    const uint32_t t_s = tmem + lanes + grp * N, t_o = tmem + lanes + (2 + grp) * N;
+    const uint32_t t_o = tmem + lanes + (AD_AHEAD + grp) * N;
     uint8_t *pm = pbuf + grp * C::P;
     const uint32_t p_off = (uint32_t)((key >> 6) * (N * 128) + (key & 7) * 2);
     const int p_chunk = (key & 63) >> 3;
     const float sc = a.scale_log2;
-    int f = 0, mine = 0, ends = 0;  // tile of the stretch, tiles of this group, its segments
+    constexpr int W = N < 32 ? N : 32;
+    int f = 0, mine = 0;  // tile of the stretch, tiles that this group has taken
     for (; s.count; s.next(a, TPB)) {
       const int nrows = s.n * a.g, pos0 = s.sp.pos0;
       float l[N];
@@ -246,48 +230,73 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
         const int lo = min(t_lo, 1 << 16) * a.g, hi = t_hi > t_lo ? t_hi * a.g : 0;
         const int j0 = (s.tile + i) * AT_KEYS;
         const bool edge = j0 + AT_KEYS - 1 > pos0 || (a.window && j0 < pos0 + s.n - a.window);
-        at_wait(&S.s_full[grp], mine & 1, &S.gave_up, a.status);
+        const uint32_t t_s = tmem + lanes + (f % AD_AHEAD) * N;
+        at_wait(&S.s_full[f % AD_AHEAD], (f / AD_AHEAD) & 1, &S.gave_up, a.status);
         tc_fence_after();
-        auto load = [&](int c0, float v[16]) {
-          tmem_ld16(t_s + c0, v);
+        // the group's last products: their probabilities' room and the sums are free once they are complete
+        bool settled = mine == 0;
+        auto settle = [&]() {
+          if (!settled) {
+            at_wait(&S.o_full[grp], (mine - 1) & 1, &S.gave_up, a.status);
+            tc_fence_after();
+          }
+          settled = true;
+        };
+        // columns c0 .. c0 + W - 1 of the scores less the running maxima, in
+        // powers of two: masked ones are -infinity whatever the key holds
+        auto load = [&](int c0, float *v) {
+          if (W == 16) tmem_ld16(t_s, v);
+          else tmem_ld32(t_s + c0, v);
+#pragma unroll
+          for (int c = 0; c < W; c += 4) {
+            const float4 m = *reinterpret_cast<const float4 *>(&S.ref[grp][c0 + c]);
+            const float2 u = fma2(make_float2(v[c], v[c + 1]), make_float2(sc, sc), make_float2(-m.x, -m.y));
+            const float2 w = fma2(make_float2(v[c + 2], v[c + 3]), make_float2(sc, sc), make_float2(-m.z, -m.w));
+            v[c] = u.x; v[c + 1] = u.y; v[c + 2] = w.x; v[c + 3] = w.y;
+          }
           if (edge) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = c0 + c >= lo && c0 + c < hi ? v[c] : -INFINITY;
+            for (int c = 0; c < W; ++c) v[c] = c0 + c >= lo && c0 + c < hi ? v[c] : -INFINITY;
           }
         };
-        bool higher = false;
+        float x[W];  // (64 columns do not fit the registers beside their sums: they are loaded again)
+        for (bool again = false;; again = true) {
+          float top = -INFINITY;
+          if (N == W || !again) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < N; c0 += W) {
+              load(c0, x);
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 16) {
-          float v[16];
-          load(c0, v);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) higher |= v[c] * sc > S.ref[grp][c0 + c] + AT_SLACK;
-        }
-        if (bar_or(1 + grp, 128, higher)) {
-          // raise the maxima to the tile's, and bring sums down to them
-          for (int c0 = 0; c0 < N; c0 += 16) {
-            float v[16];
-            load(c0, v);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float x = isnan(v[c]) ? -INFINITY : v[c] * sc;
-              const uint32_t k = __reduce_max_sync(0xffffffffu, ord_key(x));
-              if (lane == 0) S.top[grp][wq][c0 + c] = ord_val(k);
+              for (int c = 0; c < W; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
             }
+          }
+          if (again || !bar_or(1 + grp, 128, top > AT_SLACK)) break;
+          // raise the maxima to the tile's, and bring the sums down to them
+          settle();
+#pragma unroll 1
+          for (int c0 = 0; c0 < N; c0 += W) {
+            float v[W];
+            if (W == 16) tmem_ld16(t_s, v);
+            else tmem_ld32(t_s + c0, v);
+#pragma unroll
+            for (int c = 0; c < W; ++c)
+              v[c] = isnan(v[c]) || (edge && (c0 + c < lo || c0 + c >= hi)) ? -INFINITY : v[c] * sc;
+            const float t = warp_columns<W, true>(v);
+            if (lane < W) S.top[grp][wq][c0 + lane] = t;
           }
           named_bar(1 + grp, 128);
           if (key < N) {
             const float was = S.ref[grp][key];
-            const float now = fmaxf(fmaxf(fmaxf(S.top[grp][0][key], S.top[grp][1][key]),
-                                          fmaxf(S.top[grp][2][key], S.top[grp][3][key])), was);
-            S.ref[grp][key] = now;
-            S.factor[grp][key] = ex2(was - now);
+            const float to = fmaxf(fmaxf(fmaxf(S.top[grp][0][key], S.top[grp][1][key]),
+                                         fmaxf(S.top[grp][2][key], S.top[grp][3][key])), was);
+            S.ref[grp][key] = to;
+            S.factor[grp][key] = ex2(was - to);
           }
           named_bar(1 + grp, 128);
+          if (done) {
 #pragma unroll
-          for (int c = 0; c < N; ++c) l[c] *= S.factor[grp][c];
-          if (done) {  // (this group's earlier products are complete: its scores were issued behind them)
-#pragma unroll
+            for (int c = 0; c < N; ++c) l[c] *= S.factor[grp][c];
+#pragma unroll 1
             for (int c0 = 0; c0 < N; c0 += 16) {
               float o[16];
               tmem_ld16(t_o + c0, o);
@@ -299,15 +308,20 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           }
         }
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 16) {
-          float v[16];
-          load(c0, v);
+        for (int c0 = 0; c0 < N; c0 += W) {
+          if (N > W) load(c0, x);
 #pragma unroll
-          for (int c = 0; c < 16; c += 2) {
-            const float p0 = ex2(fmaf(v[c], sc, -S.ref[grp][c0 + c])), p1 = ex2(fmaf(v[c + 1], sc, -S.ref[grp][c0 + c + 1]));
-            l[c0 + c] += p0;
-            l[c0 + c + 1] += p1;
-            const uint32_t w = pack16<BF16>(p0, p1);
+          for (int c = 0; c < W; c += 2) {
+            const float p0 = ex2(x[c]), p1 = ex2(x[c + 1]);
+            const float2 t = add2(make_float2(l[c0 + c], l[c0 + c + 1]), make_float2(p0, p1));
+            l[c0 + c] = t.x;
+            l[c0 + c + 1] = t.y;
+            x[c / 2] = __uint_as_float(pack16<BF16>(p0, p1));
+          }
+          settle();
+#pragma unroll
+          for (int c = 0; c < W; c += 2) {
+            const uint32_t w = __float_as_uint(x[c / 2]);
             uint8_t *at = pm + p_off + (c0 + c) * 128;
             *reinterpret_cast<uint16_t *>(at + ((p_chunk ^ (c & 7)) << 4)) = (uint16_t)w;
             *reinterpret_cast<uint16_t *>(at + 128 + ((p_chunk ^ ((c + 1) & 7)) << 4)) = (uint16_t)(w >> 16);
@@ -318,9 +332,8 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           // take away an infinity or NaN, so rows that no token sees are
           // cleared, and what is not finite in others is added to the sums of
           // the rows that see it, and cleared
-          const int va = v_at(f);
-          at_wait(&S.full[va % SLOTS], (va / SLOTS) & 1, &S.gave_up, a.status);
-          uint8_t *vt = ring + (va % SLOTS) * C::TILE, *vr = vt + key * 128;
+          at_wait(&S.full[1][f % SLOTS], (f / SLOTS) & 1, &S.gave_up, a.status);
+          uint8_t *vt = vring + f % SLOTS * C::TILE, *vr = vt + key * 128;
           bool odd = false;
           if (hi <= lo) {
 #pragma unroll
@@ -373,13 +386,12 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
       }
       // ---- the segment's end: each group finishes half of the rows ----
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        const float t = warp_sum(l[c]);
-        if (lane == 0) S.sum[grp][wq][c] = t;
+      for (int c0 = 0; c0 < N; c0 += W) {
+        const float t = warp_columns<W, false>(l + c0);
+        if (lane < W) S.sum[grp][wq][c0 + lane] = t;
       }
       if (done) {
-        at_wait(&S.o_full[grp], ends & 1, &S.gave_up, a.status);
-        ++ends;
+        at_wait(&S.o_full[grp], (mine - 1) & 1, &S.gave_up, a.status);
         tc_fence_after();
       }
       // both groups' products are done before the probabilities' room is
@@ -387,6 +399,26 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
       named_bar(3, 256);
       float *ex = reinterpret_cast<float *>(pbuf);
       constexpr int HALF = N / 2;
+      const bool whole = s.has_start() && s.has_end();
+      const int64_t piece = 2 * (int64_t)blockIdx.x + (s.index > 0);
+      if (key < HALF && grp * HALF + key < nrows) {  // a thread a row: its weights and place
+        const int row = grp * HALF + key;
+        const float m0 = S.ref[0][row], m1 = S.ref[1][row], m = fmaxf(m0, m1), w0 = ex2(m0 - m), w1 = ex2(m1 - m);
+        const float s0 = (S.sum[0][0][row] + S.sum[0][1][row]) + (S.sum[0][2][row] + S.sum[0][3][row]);
+        const float s1 = (S.sum[1][0][row] + S.sum[1][1][row]) + (S.sum[1][2][row] + S.sum[1][3][row]);
+        const float total = s0 * w0 + s1 * w1, inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
+        S.weight[row] = make_float2((grp ? w1 : w0) * inv, (grp ? w0 : w1) * inv);
+        if (whole) {
+          const int tok = row / a.g;
+          const int64_t t = s.sp.t0 + tok;
+          const int h = s.h * a.g + row - tok * a.g;
+          S.place[row] = t * a.os + (int64_t)h * a.D;
+          if (a.lse) a.lse[t * a.H + h] = total == 0.f ? -INFINITY : (m + log2f(total)) * AT_LN2;
+        } else {
+          S.place[row] = (piece * N + row) * DP;
+          pieces.stats[piece * N + row] = make_float2(m, total);
+        }
+      }
       float o[HALF];
 #pragma unroll
       for (int c = 0; c < HALF; c += 8) tmem_ld8(t_o + (1 - grp) * HALF + c, o + c);
@@ -398,28 +430,17 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
       for (int c = 0; c < HALF; c += 8) tmem_ld8(t_o + grp * HALF + c, o + c);
       tc_fence_before();
       named_bar(3, 256);
-      const bool whole = s.has_start() && s.has_end();
-      const int64_t piece = 2 * (int64_t)blockIdx.x + (s.index > 0);
+      if (key < (whole ? a.D : DP)) {
 #pragma unroll
-      for (int c = 0; c < HALF; ++c) {
-        const int row = grp * HALF + c;
-        if (row >= nrows) continue;
-        const float m0 = S.ref[0][row], m1 = S.ref[1][row], m = fmaxf(m0, m1), w0 = ex2(m0 - m), w1 = ex2(m1 - m);
-        const float s0 = (S.sum[0][0][row] + S.sum[0][1][row]) + (S.sum[0][2][row] + S.sum[0][3][row]);
-        const float s1 = (S.sum[1][0][row] + S.sum[1][1][row]) + (S.sum[1][2][row] + S.sum[1][3][row]);
-        const float total = s0 * w0 + s1 * w1;
-        const float own = o[c];
-        if (whole) {
-          const int64_t t = s.sp.t0 + row / a.g;
-          const int h = s.h * a.g + row % a.g;
-          if (key < a.D) {
-            const float v = own * (grp ? w1 : w0) + ex[row * DP + key] * (grp ? w0 : w1);
-            a.out[t * a.os + (int64_t)h * a.D + key] = (uint16_t)pack16<BF16>(total == 0.f ? 0.f : v / total, 0.f);
+        for (int c = 0; c < HALF; ++c) {
+          const int row = grp * HALF + c;
+          if (row < nrows) {
+            const float2 w = S.weight[row];
+            // (a sum of zero keys times a weight of zero: sums are zeros then, not garbage)
+            const float v = o[c] * w.x + ex[row * DP + key] * w.y;
+            if (whole) a.out[S.place[row] + key] = (uint16_t)pack16<BF16>(v, 0.f);
+            else pieces.sums[S.place[row] + key] = v;
           }
-          if (a.lse && key == 0) a.lse[t * a.H + h] = total == 0.f ? -INFINITY : (m + log2f(total)) * AT_LN2;
-        } else {
-          if (key < DP) pieces.sums[(piece * N + row) * DP + key] = own * (grp ? w1 : w0) + ex[row * DP + key] * (grp ? w0 : w1);
-          if (key == 0) pieces.stats[piece * N + row] = make_float2(m, total);
         }
       }
       if (!whole && tid == 0)
@@ -431,14 +452,14 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
   __syncthreads();
   if (warp == AD_MMA) {
     tc_fence_after();
-    tmem_free<4 * N>(tmem);
+    tmem_free<C::TMEM>(tmem);
   }
 }
 
 template <int N, int DP, bool BF16>
 cudaError_t launch(const AttnArgs &a, void *ws, cudaStream_t s) {
   using C = AdCfg<N, DP>;
-  constexpr size_t smem = 1024 + C::SLOTS * C::TILE + 2 * (C::Q + C::P) + sizeof(AdShared<N, C::SLOTS>);
+  constexpr size_t smem = 1024 + 2 * C::SLOTS * C::TILE + 2 * (C::Q + C::P) + sizeof(AdShared<N, C::SLOTS>);
   static_assert(smem <= 227 * 1024, "shared memory of a block");
   static OncePerDevice once;
   cudaError_t e = once_per_device(once, []() {

@@ -68,6 +68,50 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Column sums (MAX: maxima) over a warp of W = 16 or 32 values a lane: lane i
+// ends with column i mod W.  Each step sends away the half of the columns
+// that the lane will not own, so it takes W - 1 shuffles (and one more for
+// 16 columns) where a butterfly for each column takes 5 W.
+template <int W, bool MAX>
+__device__ __forceinline__ float warp_columns(float v[W]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = W / 2; s > 0; s >>= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float keep = up ? v[i + s] : v[i], send = up ? v[i] : v[i + s];
+      const float got = __shfl_xor_sync(0xffffffffu, send, s);
+      v[i] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  if (W == 16) {
+    const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
+    v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
+  }
+  return v[0];
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // Two floats as 16-bit ones, a in the low half.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
@@ -86,6 +130,8 @@ __device__ __forceinline__ bool not_finite2(uint32_t w) {
   return (w & M) == M || (w & (M << 16)) == (M << 16);
 }
 
+constexpr int AT_ITEM = 2;
+
 // Tiles [begin, end) that tokens first .. first + n - 1 of a request see: one
 // at least, so that a block of tokens that sees no key is still written.
 __device__ __forceinline__ void tile_range(const Span &s, int first, int n, int window, int &begin, int &end) {
@@ -94,19 +140,21 @@ __device__ __forceinline__ void tile_range(const Span &s, int first, int n, int 
   end = max(begin + 1, (p + n + AT_KEYS - 1) / AT_KEYS);
 }
 
-__device__ __forceinline__ int64_t request_tiles(const Span &s, int tpb, int window) {
+// Length on the line of one key head's items of a request.
+__device__ __forceinline__ int64_t request_line(const Span &s, int tpb, int window) {
   int64_t sum = 0;
   for (int f = 0; f < s.n; f += tpb) {
     int b, e;
     tile_range(s, f, min(tpb, s.n - f), window, b, e);
-    sum += e - b;
+    sum += e - b + AT_ITEM;
   }
   return sum;
 }
 
-// Where a block's stretch begins, and how many tiles it has.
+// Where a block's stretch of the line begins (request, key head, block of
+// rows, place in the item), and its length.
 struct Start {
-  int r, h, b, tile;
+  int r, h, b, at;
   int64_t left;
 };
 
@@ -119,7 +167,7 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, int tpb, Start *ou
   bool bad = false;
   int64_t mine = 0;
   for (int r = r0; r < r1; ++r)
-    mine += request_tiles(request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad), tpb, a.window);
+    mine += request_line(request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad), tpb, a.window);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -136,69 +184,81 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, int tpb, Start *ou
   }
   total *= a.G;
   before *= a.G;
-  // with fewer tiles than blocks the first blocks have one each
-  const int64_t c = blockIdx.x, blocks = gridDim.x;
-  const int64_t s = total >= blocks ? total * c / blocks : min(c, total);
-  const int64_t e = total >= blocks ? total * (c + 1) / blocks : min(c + 1, total);
+  // no stretch is shorter than an item's overhead and a tile: with little to
+  // do the first blocks have a tile each
+  const int64_t c = blockIdx.x, blocks = gridDim.x, least = AT_ITEM + 1;
+  const bool full = total >= blocks * least;
+  const int64_t s = full ? total * c / blocks : min(c * least, total);
+  const int64_t e = full ? total * (c + 1) / blocks : min((c + 1) * least, total);
   if (tid == 0) out->left = e - s;
   if (s >= before && s < before + mine * a.G) {
     int64_t off = s - before;
     for (int r = r0; r < r1; ++r) {
       const Span sp = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
-      const int64_t tr = request_tiles(sp, tpb, a.window);
-      if (off >= tr * a.G) {
-        off -= tr * a.G;
+      const int64_t line = request_line(sp, tpb, a.window);
+      if (off >= line * a.G) {
+        off -= line * a.G;
         continue;
       }
       out->r = r;
-      out->h = (int)(off / tr);
-      off %= tr;
+      out->h = (int)(off / line);
+      off %= line;
       int b = 0, t0, t1;
       for (;; ++b) {
         tile_range(sp, b * tpb, min(tpb, sp.n - b * tpb), a.window, t0, t1);
-        if (off < t1 - t0) break;
-        off -= t1 - t0;
+        if (off < t1 - t0 + AT_ITEM) break;
+        off -= t1 - t0 + AT_ITEM;
       }
       out->b = b;
-      out->tile = t0 + (int)off;
+      out->at = (int)off;
       break;
     }
   }
   if (bad && blockIdx.x == 0) flag(a.status, ST_PAGING);
 }
 
-// The segments of a block's stretch, in order: runs of tiles of one item.
+// The segments of a block's stretch, in order: runs of tiles of one item
+// (none of them empty).  An item's places on the line are its overhead and
+// then its tiles.
 struct Segments {
-  int r, h, b, tile, begin, end, count, index;
+  int r, h, b, at, begin, end, tile, count, index;
   int64_t left;
   Span sp;
   // of the segment: its first token in the request, its tokens
   int first, n;
 
   __device__ __forceinline__ void init(const AttnArgs &a, int tpb, const Start &s) {
-    r = s.r; h = s.h; b = s.b; left = s.left;
+    r = s.r; h = s.h; b = s.b; at = s.at; left = s.left;
     index = 0;
+    count = 0;
     if (left > 0) {
       bool bad = false;
       sp = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
       item(a, tpb);
-      tile = s.tile;
+      if (!count) advance(a, tpb);
     }
-    size();
   }
+  // The tiles of the current item from place `at` on, as far as the stretch goes.
   __device__ __forceinline__ void item(const AttnArgs &a, int tpb) {
     first = b * tpb;
     n = min(tpb, sp.n - first);
     tile_range(sp, first, n, a.window, begin, end);
-    tile = begin;
+    tile = begin + max(0, at - AT_ITEM);
+    const int64_t stop = min(at + left, (int64_t)(end - begin + AT_ITEM));
+    count = (int)max(stop - AT_ITEM, (int64_t)0) - (tile - begin);
   }
-  __device__ __forceinline__ void size() { count = left > 0 ? (int)min(left, (int64_t)(end - tile)) : 0; }
   __device__ __forceinline__ bool has_start() const { return tile == begin; }
   __device__ __forceinline__ bool has_end() const { return tile + count == end; }
   __device__ __forceinline__ void next(const AttnArgs &a, int tpb) {
-    left -= count;
     ++index;
-    if (left > 0) {
+    advance(a, tpb);
+  }
+  __device__ __forceinline__ void advance(const AttnArgs &a, int tpb) {
+    do {
+      left -= end - begin + AT_ITEM - at;
+      at = 0;
+      count = 0;
+      if (left <= 0) return;
       if (++b * tpb >= sp.n) {
         b = 0;
         if (++h == a.G) {
@@ -207,15 +267,14 @@ struct Segments {
           do {
             if (++r >= a.R) {  // lengths that changed under the kernel
               left = 0;
-              break;
+              return;
             }
             sp = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
           } while (sp.n == 0);
         }
       }
-      if (left > 0) item(a, tpb);
-    }
-    size();
+      item(a, tpb);
+    } while (!count);
   }
 };
 
@@ -315,7 +374,8 @@ inline bool make_kv_map(CUtensorMap *m, const void *base, const AttnArgs &a, int
   const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, estr[4] = {1, 1, 1, 1};
   return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), dims,
             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            // (a head's row: 256-byte fetches of 128-byte rows would bring the next head's along)
+            a.D > 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The query rows {element, head, token}: a box is 64 elements of the g heads
@@ -342,33 +402,33 @@ inline int piece_rows(int page) {
 // The copies of one tile's keys (and later its values): lane i < 128 / rows
 // has the i-th run of rows, its page and its first row there.  Runs that no
 // token of the segment sees, and pages that are none, are filled with zeros.
+// find() starts the load of the page ids, copy() uses them: the producers
+// look a tile ahead, so that no tile waits for its page ids.
 struct TileRuns {
   int page, row;
-  __device__ __forceinline__ void find(const AttnArgs &a, const Segments &s, int tile, int rows, bool &bad) {
+  bool sees;
+  __device__ __forceinline__ void find(const AttnArgs &a, const Segments &s, int tile, int rows) {
     const int lane = threadIdx.x & 31, j = tile * AT_KEYS + lane * rows;
-    page = -1;
-    row = 0;
     const int p = s.sp.pos0 + s.first, lo = a.window ? p + 1 - a.window : 0;
-    if (lane * rows < AT_KEYS && j < p + s.n && j + rows > lo) {
+    sees = lane * rows < AT_KEYS && j < p + s.n && j + rows > lo;
+    if (sees) {
       const int col = j / a.page;
       row = j - col * a.page;
       page = a.table[s.r * a.table_stride + col];
-      if (page < 0 || page >= a.n_pages) {
-        page = -1;
-        row = 0;
-        bad = true;
-      }
     }
   }
   template <int DP>
-  __device__ __forceinline__ void copy(uint8_t *slot, const CUtensorMap *map, int head, int rows, uint64_t *full) const {
+  __device__ __forceinline__ void copy(const AttnArgs &a, uint8_t *slot, const CUtensorMap *map, int head, int rows,
+                                       uint64_t *full, bool &bad) const {
     const int lane = threadIdx.x & 31;
     if (lane == 0) mbar_arrive_expect_tx(full, AT_KEYS * DP * 2);
     __syncwarp();
     if (lane * rows < AT_KEYS) {
+      const bool there = sees && page >= 0 && page < a.n_pages;
+      bad = bad || (sees && !there);
 #pragma unroll
       for (int x = 0; x < DP; x += 64)
-        tma_load_4d(slot + x / 64 * (AT_KEYS * 128) + lane * rows * 128, map, x, row, head, page, full);
+        tma_load_4d(slot + x / 64 * (AT_KEYS * 128) + lane * rows * 128, map, x, there ? row : 0, head, there ? page : -1, full);
     }
     __syncwarp();
   }
