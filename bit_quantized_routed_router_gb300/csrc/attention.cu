@@ -116,7 +116,7 @@ bool copies_fit(const ds_moe_attn_shape &s, const ds_moe_kv_cache &c, const void
 
 int path_of(const ds_moe_attn_shape &s, const ds_moe_kv_cache &c, const void *q, int64_t q_stride, int64_t T, int32_t max_new) {
   if (!copies_fit(s, c, q, q_stride, T)) return DS_ATTN_GENERIC;
-  return (int64_t)max_new * (s.n_head / s.n_head_kv) <= AD_MAX_ROWS ? DS_ATTN_DECODE : DS_ATTN_GENERIC;
+  return (int64_t)max_new * (s.n_head / s.n_head_kv) <= AD_MAX_ROWS ? DS_ATTN_DECODE : DS_ATTN_CHUNK;
 }
 
 int launch_blocks() { return std::max(device_sms(), NUM_SMS); }
@@ -154,7 +154,8 @@ int ds_moe_attention_workspace_bytes(const ds_moe_attn_shape *shape, int32_t n_r
   if (n_requests < 0 || max_new < 0 || T < 0 || T > (1 << 24))
     return fail(err, errlen, DS_ERR_INVALID_ARG, "n_requests, T or max_new out of range");
   const int64_t rows = (int64_t)max_new * (shape->n_head / shape->n_head_kv);
-  *bytes = (attention_decode_workspace(std::min(rows, AD_MAX_ROWS), launch_blocks()) + 255) / 256 * 256;
+  const size_t need = rows <= AD_MAX_ROWS ? attention_decode_workspace(rows, launch_blocks()) : attention_chunk_workspace(launch_blocks());
+  *bytes = (need + 255) / 256 * 256;
   return DS_OK;
 }
 
@@ -200,8 +201,9 @@ int ds_moe_paged_attention(const ds_moe_attn_shape *shape, const ds_moe_kv_cache
   const bool bf16 = shape->dtype == DS_BF16;
   const cudaStream_t st = (cudaStream_t)stream;
   const int path = table_width ? path_of(*shape, *cache, q, q_stride, T, max_new) : DS_ATTN_GENERIC;
-  const cudaError_t e = path == DS_ATTN_DECODE ? launch_attention_decode(a, bf16, workspace, st)
-                                               : launch_attention_generic(a, bf16, st);
+  const cudaError_t e = path == DS_ATTN_DECODE  ? launch_attention_decode(a, bf16, workspace, st)
+                        : path == DS_ATTN_CHUNK ? launch_attention_chunk(a, bf16, workspace, st)
+                                                : launch_attention_generic(a, bf16, st);
   return e == cudaSuccess ? DS_OK : cuda_fail(err, errlen, e, "attention");
 }
 

@@ -28,6 +28,8 @@ struct AttnArgs {
 constexpr int64_t AD_MAX_ROWS = 64;
 size_t attention_decode_workspace(int64_t rows, int blocks);
 cudaError_t launch_attention_decode(const AttnArgs &a, bool bf16, void *ws, cudaStream_t s);
+size_t attention_chunk_workspace(int blocks);
+cudaError_t launch_attention_chunk(const AttnArgs &a, bool bf16, void *ws, cudaStream_t s);
 cudaError_t launch_attention_generic(const AttnArgs &a, bool bf16, cudaStream_t s);
 
 }  // namespace dsm

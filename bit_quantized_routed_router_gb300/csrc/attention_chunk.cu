@@ -1,0 +1,463 @@
+// Attention of many query rows a key head (a prompt's chunk, or chunks and
+// single tokens in one batch): bound by the matrix products and the
+// exponentials.
+//
+// A block takes 256 query rows at a time, as two tiles of 128 (whole tokens
+// with the g query heads that share a key head: row i of a tile is head
+// i mod g of token i / g), over tiles of 128 keys, which both query tiles use
+// once they are in shared memory.  Scores S = Q K^T and sums O += P V are in
+// tensor memory; the probabilities overwrite the scores there and are the
+// second product's first operand, so they never pass through shared memory.
+//
+//   two groups of four warps   one a query tile, a thread a row: maximum,
+//                   exponentials, sum of its own row, no exchange between
+//                   threads; while one group works on its scores, the
+//                   products of the other run;
+//   MMA thread      per key tile and query tile: O += P V, then the next S;
+//   two producer warps         keys (and the query rows), values;
+//   value warp      hands each tile of values to the MMA thread; in tiles
+//                   that not every row sees it clears rows that none sees and
+//                   looks for infinities and NaN in the others.
+//
+// Maxima are raised lazily (AT_SLACK), by warp.
+#include "attention_tc.cuh"
+
+namespace dsm {
+namespace {
+
+constexpr int AC_THREADS = 384;
+constexpr int AC_MMA = 8, AC_KEYS = 9, AC_VALUES = 10, AC_CHECK = 11;
+constexpr int AC_ROWS = 256;
+
+template <int DP>
+struct AcCfg {
+  static constexpr uint32_t TILE = AT_KEYS * DP * 2;  // keys, values, or a query tile
+  static constexpr int KS = DP == 128 ? 2 : 4, VS = DP == 128 ? 3 : 4;
+};
+
+template <int KS, int VS>
+struct AcShared {
+  uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
+  uint64_t v_seen[VS], v_ready[VS];  // looked at; to be multiplied
+  uint64_t added[2];                 // by group: values that are not finite are in its sums
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
+  uint32_t odd[VS][4];  // keys whose values are not all finite
+  int64_t part[AC_THREADS / 32];
+  Start start;
+  uint32_t tmem;
+  int gave_up;
+};
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(AC_THREADS, 1)
+    attention_chunk_kernel(const AttnArgs a, const Pieces pieces, const __grid_constant__ CUtensorMap tm_q,
+                           const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, int rows,
+                           int tok, bool wide_out) {
+  using C = AcCfg<DP>;
+  constexpr int KS = C::KS, VS = C::VS;
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint8_t *qbuf = smem, *kring = qbuf + 2 * C::TILE, *vring = kring + KS * C::TILE;
+  typedef AcShared<KS, VS> Sh;
+  Sh &S = *reinterpret_cast<Sh *>(vring + VS * C::TILE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tpb = 2 * tok;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  if (tid == 0) {
+    for (int i = 0; i < KS; ++i) mbar_init(&S.k_full[i], 1), mbar_init(&S.k_empty[i], 1);
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(&S.v_full[i], 1);
+      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.v_seen[i], 1);
+      mbar_init(&S.v_ready[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.added[i], 4);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.o_full[i], 1);
+      pieces.what[2 * blockIdx.x + i] = make_int4(0, 0, 0, 0);
+    }
+    mbar_init(&S.q_full, 1);
+    mbar_init(&S.q_empty, 1);
+    mbar_init(&S.drain, 1);
+    S.gave_up = 0;
+    fence_mbar_init();
+  }
+  // query rows that no copy fills stay zero
+  for (int i = tid; i < (int)(2 * C::TILE / 16); i += AC_THREADS) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  find_start<AC_THREADS>(a, tpb, &S.start, S.part);
+  if (warp == AC_MMA) tmem_alloc<512>(&S.tmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;  // scores of the query tiles at 0 and 128, sums at 256 and 384
+  Segments s;
+  s.init(a, tpb, S.start);
+  // whether some row of a segment does not see some key of a tile
+  auto edge_of = [&](const Segments &s, int first, int n, int j0) {
+    const int p = s.sp.pos0 + first;
+    return j0 + AT_KEYS - 1 > p || (a.window && j0 < p + n - a.window);
+  };
+
+  if (warp == AC_KEYS || warp == AC_VALUES) {
+    // ------------------------------------------------------------ copies --
+    const bool keys = warp == AC_KEYS;
+    const CUtensorMap *map = keys ? &tm_k : &tm_v;
+    const int slots = keys ? KS : VS;
+    uint64_t *full = keys ? S.k_full : S.v_full, *empty = keys ? S.k_empty : S.v_empty;
+    uint8_t *ring = keys ? kring : vring;
+    bool ok = true, bad = false;
+    int segs = 0, f = 0, i = 0, sl = 0, ph = 0, head = s.h;
+    TileRuns now, later;
+    if (s.count) now.find(a, s, s.tile, rows);
+    for (; s.count; ++f) {
+      if (i == 0) {
+        head = s.h;
+        if (keys) {
+          if (lane == 0 && segs && !at_wait(&S.q_empty, (segs & 1) ^ 1, &S.gave_up, a.status)) ok = false;
+          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+          if (lane == 0) {
+            const int tiles = s.n > tok ? 2 : 1;
+            mbar_arrive_expect_tx(&S.q_full, tiles * tok * a.g * DP * 2);
+            for (int w = 0; w < tiles; ++w)
+#pragma unroll
+              for (int x = 0; x < DP; x += 64)
+                tma_load_3d(qbuf + w * C::TILE + x / 64 * (128 * 128), &tm_q, x, s.h * a.g, s.sp.t0 + s.first + w * tok, &S.q_full);
+          }
+          __syncwarp();
+        }
+        ++segs;
+      }
+      if (++i == s.count) {
+        s.next(a, tpb);
+        i = 0;
+      }
+      if (s.count) later.find(a, s, s.tile + i, rows);
+      if (lane == 0 && f >= slots && !at_wait(&empty[sl], ph ^ 1, &S.gave_up, a.status)) ok = false;
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      now.copy<DP>(a, ring + sl * C::TILE, map, head, rows, &full[sl], bad);
+      now = later;
+      if (++sl == slots) sl = 0, ph ^= 1;
+    }
+    if (bad) flag(a.status, ST_PAGING);
+    if (lane == 0) {  // every copy of this warp has landed before the block ends
+      int off = 0;
+      for (int g = max(0, f - slots); g < f; ++g) at_wait(&full[g % slots], (g / slots) & 1, &off, a.status);
+      if (keys && segs) at_wait(&S.q_full, (segs - 1) & 1, &off, a.status);
+    }
+  } else if (warp == AC_CHECK) {
+    // ------------------------------------------------------------ values --
+    int f = 0, adds[2] = {0, 0};
+    for (; s.count; s.next(a, tpb)) {
+      const int p = s.sp.pos0 + s.first;
+      const int see_lo = a.window ? p + 1 - a.window : 0, see_hi = p + s.n;           // some row sees it
+      const int all_lo = a.window ? p + s.n - a.window : 0, all_hi = p + 1;           // every row sees it
+      for (int i = 0; i < s.count; ++i, ++f) {
+        const int sl = f % VS, par = (f / VS) & 1, j0 = (s.tile + i) * AT_KEYS;
+        at_wait(&S.v_full[sl], par, &S.gave_up, a.status);
+        if (edge_of(s, s.first, s.n, j0)) {
+          uint8_t *vt = vring + sl * C::TILE;
+          uint32_t any = 0, m[4];
+          for (int k = 0; k < 4; ++k) {
+            const int j = j0 + 32 * k + lane;
+            uint8_t *vr = vt + (32 * k + lane) * 128;
+            bool odd = false;
+            if (j >= see_hi || j < see_lo) {
+#pragma unroll
+              for (int x = 0; x < DP / 8; ++x)
+                *reinterpret_cast<uint4 *>(vr + x / 8 * (AT_KEYS * 128) + x % 8 * 16) = make_uint4(0, 0, 0, 0);
+            } else if (j >= all_hi || j < all_lo) {
+#pragma unroll
+              for (int x = 0; x < DP / 8; ++x) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(vr + x / 8 * (AT_KEYS * 128) + x % 8 * 16);
+                odd |= not_finite2<BF16>(w.x) || not_finite2<BF16>(w.y) || not_finite2<BF16>(w.z) || not_finite2<BF16>(w.w);
+              }
+            }
+            m[k] = __ballot_sync(0xffffffffu, odd);
+            any |= m[k];
+          }
+          if (lane == 0)
+            for (int k = 0; k < 4; ++k) S.odd[sl][k] = m[k];
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.v_seen[sl]);
+          if (any) {  // once both groups have added them to the rows that see them, they are cleared
+            for (int w = 0; w < (s.n > tok ? 2 : 1); ++w) at_wait(&S.added[w], adds[w]++ & 1, &S.gave_up, a.status);
+            for (int k = 0; k < 4; ++k) {
+              if (!(m[k] >> lane & 1u)) continue;
+              uint8_t *vr = vt + (32 * k + lane) * 128;
+              for (int x = 0; x < DP / 2; ++x) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(vr + x / 32 * (AT_KEYS * 128) + x % 32 * 4);
+                if (not_finite2<BF16>(*w & 0xFFFFu)) *w &= 0xFFFF0000u;
+                if (not_finite2<BF16>(*w & 0xFFFF0000u)) *w &= 0xFFFFu;
+              }
+            }
+            fence_proxy_async();
+            __syncwarp();
+          }
+        } else if (lane == 0) {
+          mbar_arrive(&S.v_seen[sl]);  // (its phases go with the tiles)
+        }
+        if (lane == 0) mbar_arrive(&S.v_ready[sl]);
+      }
+    }
+  } else if (warp == AC_MMA) {
+    // ----------------------------------------------------------- products --
+    if (lane == 0) {
+      const uint32_t id_s = f16_idesc(AT_KEYS, BF16), id_o = f16_idesc(DP, BF16) | IDESC_B_MN;
+      bool ok = true;
+      Segments z = s;          // of the next scores
+      int iz = 0, fz = 0;      // its tile of the segment, of the stretch
+      int ntile[2] = {0, 0};   // tiles that each group has had its products from
+      auto wait = [&](uint64_t *b, int par) {
+        if (ok && !at_wait(b, par & 1, &S.gave_up, a.status)) ok = false;
+      };
+      auto scores = [&](int w) {  // S of query tile w for tile fz
+        if (iz == 0) wait(&S.q_full, z.index);
+        wait(&S.k_full[fz % KS], fz / KS);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t qd = sw128_desc(smem_u32(qbuf + w * C::TILE)), kd = sw128_desc(smem_u32(kring + fz % KS * C::TILE));
+#pragma unroll
+        for (int x = 0; x < DP / 16; ++x) {  // (addresses in a descriptor count 16 bytes)
+          const uint32_t at = (x / 4 * (AT_KEYS * 128) + x % 4 * 32) / 16;
+          mma_f16(tmem + w * 128, qd + at, kd + at, id_s, x > 0);
+        }
+        mma_commit(&S.s_full[w]);
+      };
+      auto scored = [&]() {  // the tile's scores are all issued: on to the next
+        mma_commit(&S.k_empty[fz % KS]);
+        ++fz;
+        if (++iz == z.count) {
+          mma_commit(&S.q_empty);
+          z.next(a, tpb);
+          iz = 0;
+        }
+      };
+      if (s.count) {
+        scores(0);
+        if (z.n > tok) scores(1);
+        if (ok) scored();
+      }
+      int iv = 0;
+      for (int f = 0; ok && s.count; ++f) {
+        const bool last = iv + 1 == s.count, more = z.count > 0;
+        for (int w = 0; ok && w < 2; ++w) {
+          if (w == 0 || s.n > tok) {
+            wait(&S.p_full[w], ntile[w]++);
+            wait(&S.v_ready[f % VS], f / VS);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = sw128_mn_desc(smem_u32(vring + f % VS * C::TILE), AT_KEYS * 128);
+#pragma unroll
+            for (int x = 0; x < AT_KEYS / 16; ++x)
+              mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + x * 8, vd + x * 2048 / 16, id_o, true);
+            if (last) mma_commit(&S.o_full[w]);
+          }
+          if (more && (w == 0 || z.n > tok)) scores(w);
+        }
+        if (!ok) break;
+        mma_commit(&S.v_empty[f % VS]);
+        if (more) scored();
+        if (++iv == s.count) {
+          s.next(a, tpb);
+          iv = 0;
+        }
+      }
+      mma_commit(&S.drain);
+      int off = 0;
+      at_wait(&S.drain, 0, &off, a.status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax --
+    const int grp = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t t_s = tmem + lanes + grp * 128, t_o = tmem + lanes + 256 + grp * 128;
+    const float sc = a.scale_log2;
+    const int my_tok = row / a.g, my_head = row - my_tok * a.g;
+    int f = 0, mine = 0, ends = 0;  // tile of the stretch, tiles and segments of this group
+    for (; s.count; f += s.count, s.next(a, tpb)) {
+      const int first = s.first + grp * tok, n = min(tok, s.n - grp * tok);  // tokens of this query tile
+      if (n <= 0) continue;
+      const int pos = s.sp.pos0 + first + my_tok;  // this row's
+      const bool is_row = my_tok < n;
+      {
+        const float z[32] = {};
+#pragma unroll
+        for (int c = 0; c < DP; c += 32) tmem_st32(t_o + c, z);
+        tmem_st_wait();
+      }
+      float m = AT_NONE, l = 0.f;
+      for (int i = 0; i < s.count; ++i, ++mine) {
+        const int j0 = (s.tile + i) * AT_KEYS;
+        at_wait(&S.s_full[grp], mine & 1, &S.gave_up, a.status);
+        tc_fence_after();
+        float x[AT_KEYS];
+        tmem_ld64(t_s, x);
+        tmem_ld64(t_s + 64, x + 64);
+        // columns [lo, hi) of the tile are seen
+        const int hi = is_row ? pos + 1 - j0 : 0, lo = a.window ? pos + 1 - a.window - j0 : 0;
+        if (edge_of(s, first, n, j0)) {
+#pragma unroll
+          for (int c = 0; c < AT_KEYS; ++c) x[c] = c >= lo && c < hi ? x[c] : -INFINITY;
+        }
+        float t0 = x[0], t1 = x[1], t2 = x[2], t3 = x[3];
+#pragma unroll
+        for (int c = 4; c < AT_KEYS; c += 8) {
+          t0 = fmaxf(t0, fmaxf(x[c], x[c + 1]));
+          t1 = fmaxf(t1, fmaxf(x[c + 2], x[c + 3]));
+          if (c + 4 < AT_KEYS) {
+            t2 = fmaxf(t2, fmaxf(x[c + 4], x[c + 5]));
+            t3 = fmaxf(t3, fmaxf(x[c + 6], x[c + 7]));
+          }
+        }
+        const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sc;
+        if (__any_sync(0xffffffffu, top > m + AT_SLACK)) {
+          // raise the maximum, and bring the sums down to it (the earlier
+          // products are complete: these scores were issued behind them)
+          const float to = fmaxf(m, top), keep = ex2(m - to);
+          l *= keep;
+          m = to;
+          if (i) {
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 16) {
+              float o[16];
+              tmem_ld16(t_o + c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= keep;
+              tmem_st16(t_o + c, o);
+            }
+          }
+        }
+        const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int c = 0; c < AT_KEYS; c += 4) {
+          const float2 u = fma2(make_float2(x[c], x[c + 1]), sc2, m2), w = fma2(make_float2(x[c + 2], x[c + 3]), sc2, m2);
+          const float2 p = make_float2(ex2(u.x), ex2(u.y)), q = make_float2(ex2(w.x), ex2(w.y));
+          sum0 = add2(sum0, p);
+          sum1 = add2(sum1, q);
+          x[c / 2] = __uint_as_float(pack16<BF16>(p.x, p.y));
+          x[c / 2 + 1] = __uint_as_float(pack16<BF16>(q.x, q.y));
+          if (c == 60) tmem_st32(t_s, x);
+          if (c == 124) tmem_st32(t_s + 32, x + 32);
+        }
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+        if (edge_of(s, s.first, s.n, j0)) {
+          // values that are not finite, and that not every row sees: a
+          // probability of zero does not take them away, so the rows that see
+          // them have them added here, and the products get zeros
+          const int sl = (f + i) % VS;
+          at_wait(&S.v_seen[sl], ((f + i) / VS) & 1, &S.gave_up, a.status);
+          if (S.odd[sl][0] | S.odd[sl][1] | S.odd[sl][2] | S.odd[sl][3]) {
+            const uint8_t *vt = vring + sl * C::TILE;
+            for (int k = 0; k < AT_KEYS; ++k) {
+              if (!(S.odd[sl][k >> 5] >> (k & 31) & 1u)) continue;
+              const bool sees = k >= lo && k < hi;
+              for (int c = 0; c < DP; c += 16) {
+                float o[16];
+                tmem_ld16(t_o + c, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const int d = c + e;
+                  const uint16_t v = *reinterpret_cast<const uint16_t *>(vt + d / 64 * (AT_KEYS * 128) + k * 128 +
+                                                                         ((((d & 63) >> 3) ^ (k & 7)) << 4) + (d & 7) * 2);
+                  if (sees && not_finite2<BF16>(v)) o[e] += BF16 ? bf16_to_f32(v) : fp16_to_f32(v);
+                }
+                tmem_st16(t_o + c, o);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.added[grp]);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[grp]);
+      }
+      // ---- the segment's end ----
+      at_wait(&S.o_full[grp], ends++ & 1, &S.gave_up, a.status);
+      tc_fence_after();
+      const bool whole = s.has_start() && s.has_end();
+      const int64_t piece = 2 * (int64_t)blockIdx.x + (s.index > 0);
+      const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const int64_t t = s.sp.t0 + first + my_tok;
+      const int h = s.h * a.g + my_head;
+      uint16_t *out = a.out + t * a.os + (int64_t)h * a.D;
+      float *sums = pieces.sums + (piece * AC_ROWS + grp * 128 + row) * DP;
+      for (int c = 0; c < DP; c += 16) {
+        float o[16];
+        tmem_ld16(t_o + c, o);
+        if (!is_row) continue;
+        if (!whole) {
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4 *>(sums + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          continue;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k += 8) {
+          if (wide_out) {  // (head_dim is a multiple of 8)
+            if (c + k < a.D)
+              *reinterpret_cast<uint4 *>(out + c + k) =
+                  make_uint4(pack16<BF16>(o[k] * inv, o[k + 1] * inv), pack16<BF16>(o[k + 2] * inv, o[k + 3] * inv),
+                             pack16<BF16>(o[k + 4] * inv, o[k + 5] * inv), pack16<BF16>(o[k + 6] * inv, o[k + 7] * inv));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (c + k + e < a.D) out[c + k + e] = (uint16_t)pack16<BF16>(o[k + e] * inv, 0.f);
+          }
+        }
+      }
+      if (is_row) {
+        if (!whole) pieces.stats[piece * AC_ROWS + grp * 128 + row] = make_float2(m, l);
+        else if (a.lse) a.lse[t * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * AT_LN2;
+      }
+      if (!whole && tid == 0)
+        pieces.what[piece] = make_int4(s.r, s.h, s.b, PIECE_USED | (s.has_start() ? PIECE_START : 0) | (s.has_end() ? PIECE_END : 0));
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == AC_MMA) {
+    tc_fence_after();
+    tmem_free<512>(tmem);
+  }
+}
+
+template <int DP, bool BF16>
+cudaError_t launch(const AttnArgs &a, void *ws, cudaStream_t s) {
+  using C = AcCfg<DP>;
+  constexpr size_t smem = 1024 + (2 + C::KS + C::VS) * C::TILE + sizeof(AcShared<C::KS, C::VS>);
+  static_assert(smem <= 227 * 1024, "shared memory of a block");
+  static OncePerDevice once;
+  cudaError_t e = once_per_device(once, []() {
+    return cudaFuncSetAttribute(attention_chunk_kernel<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (e != cudaSuccess) return e;
+  const int blocks = device_sms(), rows = piece_rows(a.page), tok = 128 / a.g;
+  CUtensorMap tq, tk, tv;
+  if (!make_q_map(&tq, a, tok, BF16) || !make_kv_map(&tk, a.k, a, rows, BF16) || !make_kv_map(&tv, a.v, a, rows, BF16))
+    return cudaErrorInvalidValue;
+  const bool wide_out = ((uintptr_t)a.out % 16) == 0 && a.os % 8 == 0;
+  const Pieces p = pieces_of(ws, blocks, AC_ROWS, DP);
+  attention_chunk_kernel<DP, BF16><<<blocks, AC_THREADS, smem, s>>>(a, p, tq, tk, tv, rows, tok, wide_out);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_join<DP, BF16>(a, p, blocks, AC_ROWS, 2 * tok, tok, s);
+}
+
+}  // namespace
+
+size_t attention_chunk_workspace(int blocks) { return pieces_bytes(blocks, AC_ROWS, 128); }
+
+cudaError_t launch_attention_chunk(const AttnArgs &a, bool bf16, void *ws, cudaStream_t s) {
+  if (a.D <= 64) return bf16 ? launch<64, true>(a, ws, s) : launch<64, false>(a, ws, s);
+  return bf16 ? launch<128, true>(a, ws, s) : launch<128, false>(a, ws, s);
+}
+
+}  // namespace dsm

@@ -473,16 +473,7 @@ cudaError_t launch(const AttnArgs &a, void *ws, cudaStream_t s) {
   const Pieces p = pieces_of(ws, blocks, N, DP);
   attention_decode_kernel<N, DP, BF16><<<blocks, AD_THREADS, smem, s>>>(a, p, tq, tk, tv, rows);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks, N / 4);
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, BF16>, a, p, N, 1 << 20);
+  return launch_join<DP, BF16>(a, p, blocks, N, 1 << 20, 1 << 20, s);
 }
 
 template <int N>

@@ -303,7 +303,7 @@ inline Pieces pieces_of(void *ws, int blocks, int rows, int dp) {
 // the order of its keys.  Block x looks at the piece that block x of the
 // attention began and did not end.
 template <int DP, bool BF16>
-__global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a, const Pieces p, int rows, int tpb) {
+__global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a, const Pieces p, int rows, int tpb, int tok) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int PER = DP / 32;
@@ -315,8 +315,10 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a, c
   }
   bool bad = false;
   const Span sp = request_span(a.cu, a.seq, w.x, a.T, a.max_new, a.max_seq, bad);
-  const int first = w.z * tpb, row = blockIdx.y * 4 + warp;
-  if (row >= min(tpb, sp.n - first) * a.g) return;
+  // rows in tiles of 128, each of `tok` tokens' g heads
+  const int first = w.z * tpb, row = blockIdx.y * 4 + warp, in_tile = row % 128;
+  const int token = row / 128 * tok + in_tile / a.g;
+  if (in_tile >= tok * (int64_t)a.g || token >= min(tpb, sp.n - first)) return;
   // how many pieces: up to the block whose first piece ends the item
   int n = 1;
   for (int c = blockIdx.x + 1;; c += 32) {
@@ -352,14 +354,29 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a, c
       }
     }
   }
-  const int64_t t = sp.t0 + first + row / a.g;
-  const int h = w.y * a.g + row % a.g;
+  const int64_t t = sp.t0 + first + token;
+  const int h = w.y * a.g + in_tile % a.g;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t *out = a.out + t * a.os + (int64_t)h * a.D + PER * lane;
 #pragma unroll
   for (int i = 0; i < PER; ++i)
     if (PER * lane + i < a.D) out[i] = (uint16_t)pack16<BF16>(o[i] * inv, 0.f);
   if (a.lse && lane == 0) a.lse[t * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * AT_LN2;
+}
+
+// Behind an attention kernel of `blocks` blocks; its set-up overlaps that kernel's end.
+template <int DP, bool BF16>
+cudaError_t launch_join(const AttnArgs &a, const Pieces &p, int blocks, int rows, int tpb, int tok, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks, rows / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, BF16>, a, p, rows, tpb, tok);
 }
 
 // The keys or values as a 4-D map {element, row of a page, head, page} with
