@@ -25,7 +25,7 @@ struct AttnArgs {
 };
 
 // Query rows a key head up to which the decode kernel serves.
-constexpr int64_t AD_MAX_ROWS = 64;
+constexpr int64_t AD_MAX_ROWS = 32;
 size_t attention_decode_workspace(int64_t rows, int blocks);
 cudaError_t launch_attention_decode(const AttnArgs &a, bool bf16, void *ws, cudaStream_t s);
 size_t attention_chunk_workspace(int blocks);

@@ -9,11 +9,15 @@
 // tensor memory; the probabilities overwrite the scores there and are the
 // second product's first operand, so they never pass through shared memory.
 //
-//   two groups of four warps   one a query tile, a thread a row: maximum,
-//                   exponentials, sum of its own row, no exchange between
-//                   threads; while one group works on its scores, the
-//                   products of the other run;
-//   MMA thread      per key tile and query tile: O += P V, then the next S;
+//   two groups of four warps   a thread a query row: maximum, exponentials,
+//                   sum of its own row, no exchange between threads; while
+//                   one group works on its scores, the products of the other
+//                   run.  The groups take turns: turn j is group j mod 2's.
+//                   Where there are two query tiles, a key tile is two turns,
+//                   one a query tile; where there is one (the request's
+//                   tokens fit it), a key tile is one turn, and the groups'
+//                   sums are joined at the segment's end;
+//   MMA thread      per turn: O += P V, then S of the turn after the next;
 //   two producer warps         keys (and the query rows), values;
 //   value warp      hands each tile of values to the MMA thread; in tiles
 //                   that not every row sees it clears rows that none sees and
@@ -27,7 +31,9 @@ namespace {
 
 constexpr int AC_THREADS = 384;
 constexpr int AC_MMA = 8, AC_KEYS = 9, AC_VALUES = 10, AC_CHECK = 11;
+constexpr int AC_READERS = 11;  // warps that read the segments: all but the keys' producer
 constexpr int AC_ROWS = 256;
+constexpr int AC_HEAD = 3 * 1024;  // bytes of a block's barriers and small arrays
 
 template <int DP>
 struct AcCfg {
@@ -42,6 +48,8 @@ struct AcShared {
   uint64_t added[2];                 // by group: values that are not finite are in its sums
   uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
   uint32_t odd[VS][4];  // keys whose values are not all finite
+  float2 stats[2][128]; // maximum and sum of a row, by group
+  SegRing segs;
   int64_t part[AC_THREADS / 32];
   Start start;
   uint32_t tmem;
@@ -55,11 +63,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                            int tok, bool wide_out) {
   using C = AcCfg<DP>;
   constexpr int KS = C::KS, VS = C::VS;
-  extern __shared__ uint8_t raw[];
-  uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  uint8_t *qbuf = smem, *kring = qbuf + 2 * C::TILE, *vring = kring + KS * C::TILE;
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];  // (the period of the 128-byte swizzle)
   typedef AcShared<KS, VS> Sh;
-  Sh &S = *reinterpret_cast<Sh *>(vring + VS * C::TILE);
+  Sh &S = *reinterpret_cast<Sh *>(smem_tiles);
+  uint8_t *qbuf = smem_tiles + AC_HEAD, *kring = qbuf + 2 * C::TILE, *vring = kring + KS * C::TILE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tpb = 2 * tok;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -79,6 +86,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       mbar_init(&S.o_full[i], 1);
       pieces.what[2 * blockIdx.x + i] = make_int4(0, 0, 0, 0);
     }
+    S.segs.init(AC_READERS);
     mbar_init(&S.q_full, 1);
     mbar_init(&S.q_empty, 1);
     mbar_init(&S.drain, 1);
@@ -94,71 +102,94 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem;  // scores of the query tiles at 0 and 128, sums at 256 and 384
-  Segments s;
-  s.init(a, tpb, S.start);
-  // whether some row of a segment does not see some key of a tile
-  auto edge_of = [&](const Segments &s, int first, int n, int j0) {
-    const int p = s.sp.pos0 + first;
-    return j0 + AT_KEYS - 1 > p || (a.window && j0 < p + n - a.window);
-  };
+  // whether some of n rows' tokens, the first at position p, does not see some key of a tile
+  auto edge_of = [&](int p, int n, int j0) { return j0 + AT_KEYS - 1 > p || (a.window && j0 < p + n - a.window); };
 
-  if (warp == AC_KEYS || warp == AC_VALUES) {
-    // ------------------------------------------------------------ copies --
-    const bool keys = warp == AC_KEYS;
-    const CUtensorMap *map = keys ? &tm_k : &tm_v;
-    const int slots = keys ? KS : VS;
-    uint64_t *full = keys ? S.k_full : S.v_full, *empty = keys ? S.k_empty : S.v_empty;
-    uint8_t *ring = keys ? kring : vring;
+  if (warp == AC_KEYS) {
+    // -------------------------------- segments, query rows and keys ------
+    Segments s;
+    s.init(a, tpb, S.start);
     bool ok = true, bad = false;
-    int segs = 0, f = 0, i = 0, sl = 0, ph = 0, head = s.h;
+    int segs = 0, f = 0, i = 0;
     TileRuns now, later;
     if (s.count) now.find(a, s, s.tile, rows);
     for (; s.count; ++f) {
+      const int head = s.h;
       if (i == 0) {
-        head = s.h;
-        if (keys) {
-          if (lane == 0 && segs && !at_wait(&S.q_empty, (segs & 1) ^ 1, &S.gave_up, a.status)) ok = false;
-          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-          if (lane == 0) {
-            const int tiles = s.n > tok ? 2 : 1;
-            mbar_arrive_expect_tx(&S.q_full, tiles * tok * a.g * DP * 2);
-            for (int w = 0; w < tiles; ++w)
-#pragma unroll
-              for (int x = 0; x < DP; x += 64)
-                tma_load_3d(qbuf + w * C::TILE + x / 64 * (128 * 128), &tm_q, x, s.h * a.g, s.sp.t0 + s.first + w * tok, &S.q_full);
-          }
-          __syncwarp();
-        }
+        S.segs.put(segs, s, ok, &S.gave_up, a.status);
+        if (lane == 0 && segs && !at_wait(&S.q_empty, (segs & 1) ^ 1, &S.gave_up, a.status)) ok = false;
         ++segs;
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        if (lane == 0) {
+          const int tiles = s.n > tok ? 2 : 1;
+          mbar_arrive_expect_tx(&S.q_full, tiles * tok * a.g * DP * 2);
+          for (int w = 0; w < tiles; ++w)
+#pragma unroll
+            for (int x = 0; x < DP; x += 64)
+              tma_load_3d(qbuf + w * C::TILE + x / 64 * (128 * 128), &tm_q, x, s.h * a.g, s.sp.t0 + s.first + w * tok, &S.q_full);
+        }
+        __syncwarp();
       }
       if (++i == s.count) {
         s.next(a, tpb);
         i = 0;
       }
       if (s.count) later.find(a, s, s.tile + i, rows);
-      if (lane == 0 && f >= slots && !at_wait(&empty[sl], ph ^ 1, &S.gave_up, a.status)) ok = false;
+      const int sl = f % KS;
+      if (lane == 0 && f >= KS && !at_wait(&S.k_empty[sl], (f / KS & 1) ^ 1, &S.gave_up, a.status)) ok = false;
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      now.copy<DP>(a, ring + sl * C::TILE, map, head, rows, &full[sl], bad);
+      now.copy<DP>(a, kring + sl * C::TILE, &tm_k, head, rows, &S.k_full[sl], bad);
       now = later;
-      if (++sl == slots) sl = 0, ph ^= 1;
     }
+    S.segs.put(segs, s, false, &S.gave_up, a.status);
     if (bad) flag(a.status, ST_PAGING);
     if (lane == 0) {  // every copy of this warp has landed before the block ends
       int off = 0;
-      for (int g = max(0, f - slots); g < f; ++g) at_wait(&full[g % slots], (g / slots) & 1, &off, a.status);
-      if (keys && segs) at_wait(&S.q_full, (segs - 1) & 1, &off, a.status);
+      for (int g = max(0, f - KS); g < f; ++g) at_wait(&S.k_full[g % KS], g / KS & 1, &off, a.status);
+      if (segs && ok) at_wait(&S.q_full, (segs - 1) & 1, &off, a.status);
+    }
+  } else if (warp == AC_VALUES) {
+    // ------------------------------------------------------------ values --
+    bool ok = true, bad = false;
+    int k = 0, f = 0, i = 0;
+    TileRuns now, later;
+    Seg s = S.segs.get(0, a.status);
+    if (s.count) now.find(a, s.r, s.pos0 + s.first, s.n, s.tile, rows);
+    for (; s.count; ++f) {
+      const int head = s.h;
+      if (++i == s.count) {
+        S.segs.done(k);
+        s = S.segs.get(++k, a.status);
+        i = 0;
+      }
+      if (s.count) later.find(a, s.r, s.pos0 + s.first, s.n, s.tile + i, rows);
+      const int sl = f % VS;
+      if (lane == 0 && f >= VS && !at_wait(&S.v_empty[sl], (f / VS & 1) ^ 1, &S.gave_up, a.status)) ok = false;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (ok) now.copy<DP>(a, vring + sl * C::TILE, &tm_v, head, rows, &S.v_full[sl], bad);
+      else break;
+      now = later;
+    }
+    for (; s.count; s = S.segs.get(++k, a.status)) S.segs.done(k);  // (gave up: the others' segments go on to their end)
+    if (bad) flag(a.status, ST_PAGING);
+    if (lane == 0) {
+      int off = 0;
+      for (int g = max(0, f - VS); g < f; ++g) at_wait(&S.v_full[g % VS], g / VS & 1, &off, a.status);
     }
   } else if (warp == AC_CHECK) {
-    // ------------------------------------------------------------ values --
-    int f = 0, adds[2] = {0, 0};
-    for (; s.count; s.next(a, tpb)) {
-      const int p = s.sp.pos0 + s.first;
+    // ----------------------------------------------------- values' check --
+    int f = 0, turn = 0, adds[2] = {0, 0};
+    for (int k = 0;; ++k) {
+      const Seg s = S.segs.get(k, a.status);
+      if (!s.count) break;
+      const bool two = s.n > tok;
+      const int p = s.pos0 + s.first;
       const int see_lo = a.window ? p + 1 - a.window : 0, see_hi = p + s.n;           // some row sees it
       const int all_lo = a.window ? p + s.n - a.window : 0, all_hi = p + 1;           // every row sees it
-      for (int i = 0; i < s.count; ++i, ++f) {
+      for (int i = 0; i < s.count; ++i, ++f, turn += two ? 2 : 1) {
         const int sl = f % VS, par = (f / VS) & 1, j0 = (s.tile + i) * AT_KEYS;
         at_wait(&S.v_full[sl], par, &S.gave_up, a.status);
-        if (edge_of(s, s.first, s.n, j0)) {
+        if (edge_of(p, s.n, j0)) {
           uint8_t *vt = vring + sl * C::TILE;
           uint32_t any = 0, m[4];
           for (int k = 0; k < 4; ++k) {
@@ -184,8 +215,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.v_seen[sl]);
-          if (any) {  // once both groups have added them to the rows that see them, they are cleared
-            for (int w = 0; w < (s.n > tok ? 2 : 1); ++w) at_wait(&S.added[w], adds[w]++ & 1, &S.gave_up, a.status);
+          if (any) {  // once they are added to the rows that see them, they are cleared
+            for (int w = 0; w < 2; ++w)
+              if (two || w == (turn & 1)) at_wait(&S.added[w], adds[w]++ & 1, &S.gave_up, a.status);
             for (int k = 0; k < 4; ++k) {
               if (!(m[k] >> lane & 1u)) continue;
               uint8_t *vr = vt + (32 * k + lane) * 128;
@@ -203,69 +235,84 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         }
         if (lane == 0) mbar_arrive(&S.v_ready[sl]);
       }
+      S.segs.done(k);
     }
   } else if (warp == AC_MMA) {
     // ----------------------------------------------------------- products --
     if (lane == 0) {
       const uint32_t id_s = f16_idesc(AT_KEYS, BF16), id_o = f16_idesc(DP, BF16) | IDESC_B_MN;
       bool ok = true;
-      Segments z = s;          // of the next scores
-      int iz = 0, fz = 0;      // its tile of the segment, of the stretch
-      int ntile[2] = {0, 0};   // tiles that each group has had its products from
       auto wait = [&](uint64_t *b, int par) {
         if (ok && !at_wait(b, par & 1, &S.gave_up, a.status)) ok = false;
       };
-      auto scores = [&](int w) {  // S of query tile w for tile fz
-        if (iz == 0) wait(&S.q_full, z.index);
+      // segments of the scores and of the sums: their tiles, and whether they have two query tiles
+      int kz = 0, count_z, ks = 0, count_s;
+      bool two_z, two_s;
+      auto segment = [&](int k, int &count, bool &two) {
+        const Seg &g = S.segs.get(k, a.status);
+        count = g.count;
+        two = g.n > tok;
+      };
+      segment(0, count_z, two_z);
+      count_s = count_z;
+      two_s = two_z;
+      int jz = 0, iz = 0, fz = 0; // of the scores: turn, tile of the segment, tile of the stretch
+      bool half = false;          // whether the tile's first turn is done
+      auto scores = [&]() {
+        const int w = jz & 1, q = two_z ? w : 0;
+        if (iz == 0) wait(&S.q_full, kz);
         wait(&S.k_full[fz % KS], fz / KS);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t qd = sw128_desc(smem_u32(qbuf + w * C::TILE)), kd = sw128_desc(smem_u32(kring + fz % KS * C::TILE));
+        const uint64_t qd = sw128_desc(smem_u32(qbuf + q * C::TILE)), kd = sw128_desc(smem_u32(kring + fz % KS * C::TILE));
 #pragma unroll
         for (int x = 0; x < DP / 16; ++x) {  // (addresses in a descriptor count 16 bytes)
           const uint32_t at = (x / 4 * (AT_KEYS * 128) + x % 4 * 32) / 16;
           mma_f16(tmem + w * 128, qd + at, kd + at, id_s, x > 0);
         }
         mma_commit(&S.s_full[w]);
-      };
-      auto scored = [&]() {  // the tile's scores are all issued: on to the next
+        ++jz;
+        half = two_z && !half;
+        if (half) return;
         mma_commit(&S.k_empty[fz % KS]);
         ++fz;
-        if (++iz == z.count) {
+        if (++iz == count_z) {
           mma_commit(&S.q_empty);
-          z.next(a, tpb);
+          segment(++kz, count_z, two_z);
           iz = 0;
         }
       };
-      if (s.count) {
-        scores(0);
-        if (z.n > tok) scores(1);
-        if (ok) scored();
-      }
-      int iv = 0;
-      for (int f = 0; ok && s.count; ++f) {
-        const bool last = iv + 1 == s.count, more = z.count > 0;
-        for (int w = 0; ok && w < 2; ++w) {
-          if (w == 0 || s.n > tok) {
-            wait(&S.p_full[w], ntile[w]++);
-            wait(&S.v_ready[f % VS], f / VS);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t vd = sw128_mn_desc(smem_u32(vring + f % VS * C::TILE), AT_KEYS * 128);
-#pragma unroll
-            for (int x = 0; x < AT_KEYS / 16; ++x)
-              mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + x * 8, vd + x * 2048 / 16, id_o, true);
-            if (last) mma_commit(&S.o_full[w]);
-          }
-          if (more && (w == 0 || z.n > tok)) scores(w);
-        }
+      for (int j = 0; ok && j < 2 && count_z; ++j) scores();
+      int f = 0, i = 0;
+      bool half_v = false;
+      for (int j = 0; ok && count_s; ++j) {
+        const int w = j & 1;
+        wait(&S.p_full[w], j >> 1);
+        wait(&S.v_ready[f % VS], f / VS);
         if (!ok) break;
-        mma_commit(&S.v_empty[f % VS]);
-        if (more) scored();
-        if (++iv == s.count) {
-          s.next(a, tpb);
-          iv = 0;
+        tc_fence_after();
+        const uint64_t vd = sw128_mn_desc(smem_u32(vring + f % VS * C::TILE), AT_KEYS * 128);
+#pragma unroll
+        for (int x = 0; x < AT_KEYS / 16; ++x)
+          mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + x * 8, vd + x * 2048 / 16, id_o, true);
+        if (i + (two_s ? 1 : 2) >= count_s) mma_commit(&S.o_full[w]);  // the group's last turn of the segment
+        half_v = two_s && !half_v;
+        bool over = false;
+        if (!half_v) {
+          mma_commit(&S.v_empty[f % VS]);
+          ++f;
+          over = ++i == count_s;
         }
+        if (count_z) scores();
+        if (over) {
+          mbar_arrive(&S.segs.empty[ks % AT_SEGS]);
+          segment(++ks, count_s, two_s);
+          i = 0;
+        }
+      }
+      while (count_s) {  // (gave up)
+        mbar_arrive(&S.segs.empty[ks % AT_SEGS]);
+        segment(++ks, count_s, two_s);
       }
       mma_commit(&S.drain);
       int off = 0;
@@ -279,12 +326,17 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     const uint32_t t_s = tmem + lanes + grp * 128, t_o = tmem + lanes + 256 + grp * 128;
     const float sc = a.scale_log2;
     const int my_tok = row / a.g, my_head = row - my_tok * a.g;
-    int f = 0, mine = 0, ends = 0;  // tile of the stretch, tiles and segments of this group
-    for (; s.count; f += s.count, s.next(a, tpb)) {
-      const int first = s.first + grp * tok, n = min(tok, s.n - grp * tok);  // tokens of this query tile
-      if (n <= 0) continue;
-      const int pos = s.sp.pos0 + first + my_tok;  // this row's
+    int f = 0, turn = 0, mine = 0, ends = 0;  // tile and turn of the stretch; turns and segments of this group
+    for (int ks = 0;; ++ks) {
+      const Seg &s = S.segs.get(ks, a.status);
+      const int count = s.count;
+      if (!count) break;
+      const bool two = s.n > tok;
+      const int skip = two ? grp * tok : 0, n = min(tok, s.n - skip);  // the query tile's tokens
+      const int p0 = s.pos0 + s.first, n0 = s.n;                      // the segment's
+      const int pos = p0 + skip + my_tok;                             // this row's
       const bool is_row = my_tok < n;
+      int j0 = s.tile * AT_KEYS;
       {
         const float z[32] = {};
 #pragma unroll
@@ -292,19 +344,30 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         tmem_st_wait();
       }
       float m = AT_NONE, l = 0.f;
-      for (int i = 0; i < s.count; ++i, ++mine) {
-        const int j0 = (s.tile + i) * AT_KEYS;
+      int done = 0;
+      for (int i = 0; i < count; ++i, j0 += AT_KEYS, ++f) {
+        turn += two ? 2 : 1;
+        if (!two && ((turn - 1) & 1) != grp) continue;
         at_wait(&S.s_full[grp], mine & 1, &S.gave_up, a.status);
         tc_fence_after();
+        // columns [lo, hi) of the tile are seen; the others' scores are
+        // replaced in tensor memory (a short loop: the code of the common
+        // path has to stay in the instruction cache)
+        const int hi = is_row ? pos + 1 - j0 : 0, lo = a.window ? pos + 1 - a.window - j0 : 0;
+        if (edge_of(p0 + skip, n, j0)) {
+#pragma unroll 1
+          for (int c = 0; c < AT_KEYS; c += 16) {
+            float v[16];
+            tmem_ld16(t_s + c, v);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = c + k >= lo && c + k < hi ? v[k] : -INFINITY;
+            tmem_st16(t_s + c, v);
+          }
+          tmem_st_wait();
+        }
         float x[AT_KEYS];
         tmem_ld64(t_s, x);
         tmem_ld64(t_s + 64, x + 64);
-        // columns [lo, hi) of the tile are seen
-        const int hi = is_row ? pos + 1 - j0 : 0, lo = a.window ? pos + 1 - a.window - j0 : 0;
-        if (edge_of(s, first, n, j0)) {
-#pragma unroll
-          for (int c = 0; c < AT_KEYS; ++c) x[c] = c >= lo && c < hi ? x[c] : -INFINITY;
-        }
         float t0 = x[0], t1 = x[1], t2 = x[2], t3 = x[3];
 #pragma unroll
         for (int c = 4; c < AT_KEYS; c += 8) {
@@ -322,7 +385,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
           const float to = fmaxf(m, top), keep = ex2(m - to);
           l *= keep;
           m = to;
-          if (i) {
+          if (done) {
 #pragma unroll 1
             for (int c = 0; c < DP; c += 16) {
               float o[16];
@@ -347,12 +410,12 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
           if (c == 124) tmem_st32(t_s + 32, x + 32);
         }
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-        if (edge_of(s, s.first, s.n, j0)) {
+        if (edge_of(p0, n0, j0)) {
           // values that are not finite, and that not every row sees: a
           // probability of zero does not take them away, so the rows that see
           // them have them added here, and the products get zeros
-          const int sl = (f + i) % VS;
-          at_wait(&S.v_seen[sl], ((f + i) / VS) & 1, &S.gave_up, a.status);
+          const int sl = f % VS;
+          at_wait(&S.v_seen[sl], f / VS & 1, &S.gave_up, a.status);
           if (S.odd[sl][0] | S.odd[sl][1] | S.odd[sl][2] | S.odd[sl][3]) {
             const uint8_t *vt = vring + sl * C::TILE;
             for (int k = 0; k < AT_KEYS; ++k) {
@@ -379,20 +442,50 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full[grp]);
+        ++mine;
+        ++done;
       }
       // ---- the segment's end ----
-      at_wait(&S.o_full[grp], ends++ & 1, &S.gave_up, a.status);
-      tc_fence_after();
-      const bool whole = s.has_start() && s.has_end();
-      const int64_t piece = 2 * (int64_t)blockIdx.x + (s.index > 0);
+      if (done) {
+        at_wait(&S.o_full[grp], ends++ & 1, &S.gave_up, a.status);
+        tc_fence_after();
+      }
+      const bool whole = (s.flags & (SEG_START | SEG_END)) == (SEG_START | SEG_END);
+      const int64_t piece = 2 * (int64_t)blockIdx.x + (s.flags & SEG_LATER ? 1 : 0);
+      // one query tile: each group joins both groups' sums (a row's are in
+      // the same lanes of tensor memory) for half of the columns
+      float scale = 1.f, other = 0.f;
+      if (!two) {
+        S.stats[grp][row] = make_float2(m, l);
+        tc_fence_before();
+        named_bar(1, 256);
+        tc_fence_after();
+        const float2 o = S.stats[1 - grp][row];
+        const float to = fmaxf(m, o.x);
+        scale = ex2(m - to);
+        other = ex2(o.x - to);
+        l = grp ? o.y * other + l * scale : l * scale + o.y * other;
+        m = to;
+      }
       const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      const int64_t t = s.sp.t0 + first + my_tok;
+      scale *= inv;
+      other *= inv;
+      const int64_t t = s.t0 + s.first + skip + my_tok;
       const int h = s.h * a.g + my_head;
+      const int c0 = two ? 0 : grp * (DP / 2), c1 = two ? DP : c0 + DP / 2;
       uint16_t *out = a.out + t * a.os + (int64_t)h * a.D;
-      float *sums = pieces.sums + (piece * AC_ROWS + grp * 128 + row) * DP;
-      for (int c = 0; c < DP; c += 16) {
+      float *sums = pieces.sums + (piece * AC_ROWS + (two ? grp * 128 : 0) + row) * DP;
+      for (int c = c0; c < c1; c += 16) {
         float o[16];
         tmem_ld16(t_o + c, o);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] *= scale;
+        if (!two) {
+          float p[16];
+          tmem_ld16(tmem + lanes + 256 + (1 - grp) * 128 + c, p);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = fmaf(p[k], other, o[k]);
+        }
         if (!is_row) continue;
         if (!whole) {
 #pragma unroll
@@ -404,22 +497,24 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
           if (wide_out) {  // (head_dim is a multiple of 8)
             if (c + k < a.D)
               *reinterpret_cast<uint4 *>(out + c + k) =
-                  make_uint4(pack16<BF16>(o[k] * inv, o[k + 1] * inv), pack16<BF16>(o[k + 2] * inv, o[k + 3] * inv),
-                             pack16<BF16>(o[k + 4] * inv, o[k + 5] * inv), pack16<BF16>(o[k + 6] * inv, o[k + 7] * inv));
+                  make_uint4(pack16<BF16>(o[k], o[k + 1]), pack16<BF16>(o[k + 2], o[k + 3]),
+                             pack16<BF16>(o[k + 4], o[k + 5]), pack16<BF16>(o[k + 6], o[k + 7]));
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (c + k + e < a.D) out[c + k + e] = (uint16_t)pack16<BF16>(o[k + e] * inv, 0.f);
+              if (c + k + e < a.D) out[c + k + e] = (uint16_t)pack16<BF16>(o[k + e], 0.f);
           }
         }
       }
-      if (is_row) {
-        if (!whole) pieces.stats[piece * AC_ROWS + grp * 128 + row] = make_float2(m, l);
+      if (is_row && (two || grp == 0)) {
+        if (!whole) pieces.stats[piece * AC_ROWS + (two ? grp * 128 : 0) + row] = make_float2(m, l);
         else if (a.lse) a.lse[t * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * AT_LN2;
       }
       if (!whole && tid == 0)
-        pieces.what[piece] = make_int4(s.r, s.h, s.b, PIECE_USED | (s.has_start() ? PIECE_START : 0) | (s.has_end() ? PIECE_END : 0));
+        pieces.what[piece] = make_int4(s.r, s.h, s.b, PIECE_USED | (s.flags & SEG_START ? PIECE_START : 0) | (s.flags & SEG_END ? PIECE_END : 0));
       tc_fence_before();
+      S.segs.done(ks);
+      if (!two) named_bar(1, 256);  // both have read both's sums
     }
   }
   tc_fence_before();
@@ -433,7 +528,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
 template <int DP, bool BF16>
 cudaError_t launch(const AttnArgs &a, void *ws, cudaStream_t s) {
   using C = AcCfg<DP>;
-  constexpr size_t smem = 1024 + (2 + C::KS + C::VS) * C::TILE + sizeof(AcShared<C::KS, C::VS>);
+  constexpr size_t smem = AC_HEAD + (2 + C::KS + C::VS) * C::TILE;
+  static_assert(sizeof(AcShared<C::KS, C::VS>) <= AC_HEAD, "head of a block's shared memory");
   static_assert(smem <= 227 * 1024, "shared memory of a block");
   static OncePerDevice once;
   cudaError_t e = once_per_device(once, []() {

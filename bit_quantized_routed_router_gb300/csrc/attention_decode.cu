@@ -4,7 +4,7 @@
 //
 // The keys are the rows of the tensor-core tiles and the queries their
 // columns: S^T = K Q^T is 128 keys x N, O^T += V^T P^T is head_dim x N, with
-// N = 16, 32 or 64, so the work of the softmax and of the matrix products
+// N = 16 or 32, so the work of the softmax and of the matrix products
 // goes with the query rows there are, not with a tile of 128 of them.  A
 // block is
 //
@@ -33,7 +33,7 @@ template <int N, int DP>
 struct AdCfg {
   static constexpr uint32_t TILE = AT_KEYS * DP * 2;
   static constexpr uint32_t Q = N * DP * 2, P = N * AT_KEYS * 2;
-  static constexpr int TMEM = N == 64 ? 512 : 8 * N;  // columns: four tiles' scores, two groups' sums
+  static constexpr int TMEM = 8 * N;  // columns: four tiles' scores, two groups' sums
   static constexpr int ROOM = 227 * 1024 - 1024 - 2 * (Q + P) - 8192;
   static constexpr int SLOTS = ROOM / (2 * (int)TILE) < 6 ? ROOM / (2 * (int)TILE) : 6;  // of keys, and of values
 };
@@ -205,7 +205,6 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
     const uint32_t p_off = (uint32_t)((key >> 6) * (N * 128) + (key & 7) * 2);
     const int p_chunk = (key & 63) >> 3;
     const float sc = a.scale_log2;
-    constexpr int W = N < 32 ? N : 32;
     int f = 0, mine = 0;  // tile of the stretch, tiles that this group has taken
     for (; s.count; s.next(a, TPB)) {
       const int nrows = s.n * a.g, pos0 = s.sp.pos0;
@@ -242,48 +241,36 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           }
           settled = true;
         };
-        // columns c0 .. c0 + W - 1 of the scores less the running maxima, in
-        // powers of two: masked ones are -infinity whatever the key holds
-        auto load = [&](int c0, float *v) {
-          if (W == 16) tmem_ld16(t_s, v);
-          else tmem_ld32(t_s + c0, v);
+        // the scores less the running maxima, in powers of two: masked ones
+        // are -infinity whatever the key holds
+        float x[N];
+        for (bool again = false;; again = true) {
+          if (N == 16) tmem_ld16(t_s, x);
+          else tmem_ld32(t_s, x);
 #pragma unroll
-          for (int c = 0; c < W; c += 4) {
-            const float4 m = *reinterpret_cast<const float4 *>(&S.ref[grp][c0 + c]);
-            const float2 u = fma2(make_float2(v[c], v[c + 1]), make_float2(sc, sc), make_float2(-m.x, -m.y));
-            const float2 w = fma2(make_float2(v[c + 2], v[c + 3]), make_float2(sc, sc), make_float2(-m.z, -m.w));
-            v[c] = u.x; v[c + 1] = u.y; v[c + 2] = w.x; v[c + 3] = w.y;
+          for (int c = 0; c < N; c += 4) {
+            const float4 m = *reinterpret_cast<const float4 *>(&S.ref[grp][c]);
+            const float2 u = fma2(make_float2(x[c], x[c + 1]), make_float2(sc, sc), make_float2(-m.x, -m.y));
+            const float2 w = fma2(make_float2(x[c + 2], x[c + 3]), make_float2(sc, sc), make_float2(-m.z, -m.w));
+            x[c] = u.x; x[c + 1] = u.y; x[c + 2] = w.x; x[c + 3] = w.y;
           }
           if (edge) {
 #pragma unroll
-            for (int c = 0; c < W; ++c) v[c] = c0 + c >= lo && c0 + c < hi ? v[c] : -INFINITY;
+            for (int c = 0; c < N; ++c) x[c] = c >= lo && c < hi ? x[c] : -INFINITY;
           }
-        };
-        float x[W];  // (64 columns do not fit the registers beside their sums: they are loaded again)
-        for (bool again = false;; again = true) {
           float top = -INFINITY;
-          if (N == W || !again) {
-#pragma unroll 1
-            for (int c0 = 0; c0 < N; c0 += W) {
-              load(c0, x);
 #pragma unroll
-              for (int c = 0; c < W; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
-            }
-          }
+          for (int c = 0; c < N; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
           if (again || !bar_or(1 + grp, 128, top > AT_SLACK)) break;
           // raise the maxima to the tile's, and bring the sums down to them
           settle();
-#pragma unroll 1
-          for (int c0 = 0; c0 < N; c0 += W) {
-            float v[W];
-            if (W == 16) tmem_ld16(t_s, v);
-            else tmem_ld32(t_s + c0, v);
+          float v[N];
+          if (N == 16) tmem_ld16(t_s, v);
+          else tmem_ld32(t_s, v);
 #pragma unroll
-            for (int c = 0; c < W; ++c)
-              v[c] = isnan(v[c]) || (edge && (c0 + c < lo || c0 + c >= hi)) ? -INFINITY : v[c] * sc;
-            const float t = warp_columns<W, true>(v);
-            if (lane < W) S.top[grp][wq][c0 + lane] = t;
-          }
+          for (int c = 0; c < N; ++c) v[c] = isnan(v[c]) || (edge && (c < lo || c >= hi)) ? -INFINITY : v[c] * sc;
+          const float t = warp_columns<N, true>(v);
+          if (lane < N) S.top[grp][wq][lane] = t;
           named_bar(1 + grp, 128);
           if (key < N) {
             const float was = S.ref[grp][key];
@@ -308,24 +295,20 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           }
         }
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += W) {
-          if (N > W) load(c0, x);
+        for (int c = 0; c < N; c += 2) {
+          const float p0 = ex2(x[c]), p1 = ex2(x[c + 1]);
+          const float2 t = add2(make_float2(l[c], l[c + 1]), make_float2(p0, p1));
+          l[c] = t.x;
+          l[c + 1] = t.y;
+          x[c / 2] = __uint_as_float(pack16<BF16>(p0, p1));
+        }
+        settle();
 #pragma unroll
-          for (int c = 0; c < W; c += 2) {
-            const float p0 = ex2(x[c]), p1 = ex2(x[c + 1]);
-            const float2 t = add2(make_float2(l[c0 + c], l[c0 + c + 1]), make_float2(p0, p1));
-            l[c0 + c] = t.x;
-            l[c0 + c + 1] = t.y;
-            x[c / 2] = __uint_as_float(pack16<BF16>(p0, p1));
-          }
-          settle();
-#pragma unroll
-          for (int c = 0; c < W; c += 2) {
-            const uint32_t w = __float_as_uint(x[c / 2]);
-            uint8_t *at = pm + p_off + (c0 + c) * 128;
-            *reinterpret_cast<uint16_t *>(at + ((p_chunk ^ (c & 7)) << 4)) = (uint16_t)w;
-            *reinterpret_cast<uint16_t *>(at + 128 + ((p_chunk ^ ((c + 1) & 7)) << 4)) = (uint16_t)(w >> 16);
-          }
+        for (int c = 0; c < N; c += 2) {
+          const uint32_t w = __float_as_uint(x[c / 2]);
+          uint8_t *at = pm + p_off + c * 128;
+          *reinterpret_cast<uint16_t *>(at + ((p_chunk ^ (c & 7)) << 4)) = (uint16_t)w;
+          *reinterpret_cast<uint16_t *>(at + 128 + ((p_chunk ^ ((c + 1) & 7)) << 4)) = (uint16_t)(w >> 16);
         }
         if (edge) {
           // values that not every row sees: a probability of zero does not
@@ -385,10 +368,9 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
         ++done;
       }
       // ---- the segment's end: each group finishes half of the rows ----
-#pragma unroll
-      for (int c0 = 0; c0 < N; c0 += W) {
-        const float t = warp_columns<W, false>(l + c0);
-        if (lane < W) S.sum[grp][wq][c0 + lane] = t;
+      {
+        const float t = warp_columns<N, false>(l);
+        if (lane < N) S.sum[grp][wq][lane] = t;
       }
       if (done) {
         at_wait(&S.o_full[grp], (mine - 1) & 1, &S.gave_up, a.status);
@@ -482,7 +464,7 @@ cudaError_t launch_n(const AttnArgs &a, bool bf16, void *ws, cudaStream_t s) {
   return bf16 ? launch<N, 128, true>(a, ws, s) : launch<N, 128, false>(a, ws, s);
 }
 
-int columns(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int columns(int64_t rows) { return rows <= 16 ? 16 : 32; }
 
 }  // namespace
 
@@ -490,7 +472,7 @@ size_t attention_decode_workspace(int64_t rows, int blocks) { return pieces_byte
 
 cudaError_t launch_attention_decode(const AttnArgs &a, bool bf16, void *ws, cudaStream_t s) {
   const int n = columns((int64_t)a.max_new * a.g);
-  return n == 16 ? launch_n<16>(a, bf16, ws, s) : n == 32 ? launch_n<32>(a, bf16, ws, s) : launch_n<64>(a, bf16, ws, s);
+  return n == 16 ? launch_n<16>(a, bf16, ws, s) : launch_n<32>(a, bf16, ws, s);
 }
 
 }  // namespace dsm

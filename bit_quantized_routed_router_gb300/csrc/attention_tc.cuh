@@ -278,6 +278,47 @@ struct Segments {
   }
 };
 
+// A segment as one warp of a block publishes it to the others, in shared
+// memory; count 0 ends the stretch.  A ring of them: `full` is the
+// publisher's, `empty` has an arrival of every reading warp.
+constexpr int AT_SEGS = 8;
+struct Seg {
+  int r, h, b, tile, count, first, n, pos0, t0, flags;
+};
+constexpr int SEG_START = 1, SEG_END = 2, SEG_LATER = 4;  // has the item's first tile, its last; is not the stretch's first
+struct SegRing {
+  Seg seg[AT_SEGS];
+  uint64_t full[AT_SEGS], empty[AT_SEGS];
+  __device__ __forceinline__ void init(int readers) {
+    for (int i = 0; i < AT_SEGS; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], readers);
+  }
+  // By one whole warp; the k-th of the stretch.
+  __device__ __forceinline__ void put(int k, const Segments &s, bool ok, int *gave_up, unsigned *status) {
+    const int i = k % AT_SEGS;
+    if ((threadIdx.x & 31) == 0) {
+      if (k >= AT_SEGS) at_wait(&empty[i], (k / AT_SEGS & 1) ^ 1, gave_up, status);
+      Seg &g = seg[i];
+      g.r = s.r; g.h = s.h; g.b = s.b; g.tile = s.tile; g.first = s.first; g.n = s.n;
+      g.pos0 = s.sp.pos0; g.t0 = s.sp.t0;
+      g.count = ok ? s.count : 0;
+      g.flags = (s.has_start() ? SEG_START : 0) | (s.has_end() ? SEG_END : 0) | (s.index ? SEG_LATER : 0);
+      mbar_arrive(&full[i]);
+    }
+    __syncwarp();
+  }
+  // Readers wait for the publisher alone, whatever else has run out: it ends
+  // the stretch by itself then, at the same segment for all of them.
+  __device__ __forceinline__ const Seg &get(int k, unsigned *status) {
+    int never = 0;
+    for (int turns = 0; turns < 8 && !at_wait(&full[k % AT_SEGS], k / AT_SEGS & 1, &never, status); ++turns) never = 0;
+    return seg[k % AT_SEGS];
+  }
+  __device__ __forceinline__ void done(int k) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[k % AT_SEGS]);
+  }
+};
+
 // Pieces: two a block, described by (r, h, b, flags), with `rows` rows of DP
 // sums, and each row's maximum and sum of probabilities.
 constexpr int PIECE_USED = 1, PIECE_START = 2, PIECE_END = 4;
@@ -424,15 +465,19 @@ inline int piece_rows(int page) {
 struct TileRuns {
   int page, row;
   bool sees;
-  __device__ __forceinline__ void find(const AttnArgs &a, const Segments &s, int tile, int rows) {
+  // (r, n tokens from position p on: of the segment)
+  __device__ __forceinline__ void find(const AttnArgs &a, int r, int p, int n, int tile, int rows) {
     const int lane = threadIdx.x & 31, j = tile * AT_KEYS + lane * rows;
-    const int p = s.sp.pos0 + s.first, lo = a.window ? p + 1 - a.window : 0;
-    sees = lane * rows < AT_KEYS && j < p + s.n && j + rows > lo;
+    const int lo = a.window ? p + 1 - a.window : 0;
+    sees = lane * rows < AT_KEYS && j < p + n && j + rows > lo;
     if (sees) {
       const int col = j / a.page;
       row = j - col * a.page;
-      page = a.table[s.r * a.table_stride + col];
+      page = a.table[r * a.table_stride + col];
     }
+  }
+  __device__ __forceinline__ void find(const AttnArgs &a, const Segments &s, int tile, int rows) {
+    find(a, s.r, s.sp.pos0 + s.first, s.n, tile, rows);
   }
   template <int DP>
   __device__ __forceinline__ void copy(const AttnArgs &a, uint8_t *slot, const CUtensorMap *map, int head, int rows,
