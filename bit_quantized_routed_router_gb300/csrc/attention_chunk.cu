@@ -19,9 +19,12 @@
 //                   sums are joined at the segment's end;
 //   MMA thread      per turn: O += P V, then S of the turn after the next;
 //   two producer warps         keys (and the query rows), values;
-//   value warp      hands each tile of values to the MMA thread; in tiles
-//                   that not every row sees it clears rows that none sees and
-//                   looks for infinities and NaN in the others.
+//   gate warp       in tiles that not every row sees it clears the values that
+//                   none sees and looks for infinities and NaN in the others;
+//                   and it waits for a turn's values in the MMA thread's
+//                   place, as one more arrival beside the probabilities': the
+//                   products stand still while the thread that issues them
+//                   waits (about 100 cycles for a barrier that is complete).
 //
 // Maxima are raised lazily (AT_SLACK), by warp.
 #include "attention_tc.cuh"
@@ -30,7 +33,7 @@ namespace dsm {
 namespace {
 
 constexpr int AC_THREADS = 384;
-constexpr int AC_MMA = 8, AC_KEYS = 9, AC_VALUES = 10, AC_CHECK = 11;
+constexpr int AC_MMA = 8, AC_KEYS = 9, AC_VALUES = 10, AC_GATE = 11;
 constexpr int AC_READERS = 11;  // warps that read the segments: all but the keys' producer
 constexpr int AC_ROWS = 256;
 constexpr int AC_HEAD = 3 * 1024;  // bytes of a block's barriers and small arrays
@@ -44,7 +47,7 @@ struct AcCfg {
 template <int KS, int VS>
 struct AcShared {
   uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
-  uint64_t v_seen[VS], v_ready[VS];  // looked at; to be multiplied
+  uint64_t v_seen[VS];               // looked at
   uint64_t added[2];                 // by group: values that are not finite are in its sums
   uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
   uint32_t odd[VS][4];  // keys whose values are not all finite
@@ -54,6 +57,29 @@ struct AcShared {
   Start start;
   uint32_t tmem;
   int gave_up;
+};
+
+// The walk over turns that the scores take, two turns ahead of the sums.
+struct Ahead {
+  int k, count, i, f;  // segment, its tiles, tile of it, tile of the stretch
+  bool two, half;      // two turns a tile; the first of them is done
+  __device__ __forceinline__ void segment(SegRing &ring, int index, int tok, unsigned *status) {
+    const Seg &g = ring.get(index, status);
+    k = index;
+    count = g.count;
+    two = g.n > tok;
+    i = 0;
+  }
+  // To the next turn; whether the tile's, and the segment's, last one was left.
+  __device__ __forceinline__ int step(SegRing &ring, int tok, unsigned *status) {
+    if (!count) return 0;
+    half = two && !half;
+    if (half) return 0;
+    ++f;
+    if (++i < count) return 1;
+    segment(ring, k + 1, tok, status);
+    return 2;
+  }
 };
 
 template <int DP, bool BF16>
@@ -77,12 +103,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       mbar_init(&S.v_full[i], 1);
       mbar_init(&S.v_empty[i], 1);
       mbar_init(&S.v_seen[i], 1);
-      mbar_init(&S.v_ready[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.added[i], 4);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.p_full[i], 5);
       mbar_init(&S.o_full[i], 1);
       pieces.what[2 * blockIdx.x + i] = make_int4(0, 0, 0, 0);
     }
@@ -97,6 +122,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
   for (int i = tid; i < (int)(2 * C::TILE / 16); i += AC_THREADS) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
   find_start<AC_THREADS>(a, tpb, &S.start, S.part);
+  __syncwarp();
   if (warp == AC_MMA) tmem_alloc<512>(&S.tmem);
   tc_fence_before();
   __syncthreads();
@@ -176,8 +202,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       int off = 0;
       for (int g = max(0, f - VS); g < f; ++g) at_wait(&S.v_full[g % VS], g / VS & 1, &off, a.status);
     }
-  } else if (warp == AC_CHECK) {
-    // ----------------------------------------------------- values' check --
+  } else if (warp == AC_GATE) {
+    // --------------------------------------------------------------- gate --
     int f = 0, turn = 0, adds[2] = {0, 0};
     for (int k = 0;; ++k) {
       const Seg s = S.segs.get(k, a.status);
@@ -233,7 +259,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         } else if (lane == 0) {
           mbar_arrive(&S.v_seen[sl]);  // (its phases go with the tiles)
         }
-        if (lane == 0) mbar_arrive(&S.v_ready[sl]);
+        for (int t = 0; t < (two ? 2 : 1); ++t) {
+          const int j = turn + t, w = j & 1;
+          if (j >= 2) at_wait(&S.p_full[w], ((j >> 1) - 1) & 1, &S.gave_up, a.status);  // the arrival is for this turn
+          if (lane == 0) mbar_arrive(&S.p_full[w]);
+        }
       }
       S.segs.done(k);
     }
@@ -245,50 +275,35 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       auto wait = [&](uint64_t *b, int par) {
         if (ok && !at_wait(b, par & 1, &S.gave_up, a.status)) ok = false;
       };
-      // segments of the scores and of the sums: their tiles, and whether they have two query tiles
-      int kz = 0, count_z, ks = 0, count_s;
-      bool two_z, two_s;
-      auto segment = [&](int k, int &count, bool &two) {
-        const Seg &g = S.segs.get(k, a.status);
-        count = g.count;
-        two = g.n > tok;
-      };
-      segment(0, count_z, two_z);
-      count_s = count_z;
-      two_s = two_z;
-      int jz = 0, iz = 0, fz = 0; // of the scores: turn, tile of the segment, tile of the stretch
-      bool half = false;          // whether the tile's first turn is done
-      auto scores = [&]() {
-        const int w = jz & 1, q = two_z ? w : 0;
-        if (iz == 0) wait(&S.q_full, kz);
-        wait(&S.k_full[fz % KS], fz / KS);
+      Ahead z{};
+      z.segment(S.segs, 0, tok, a.status);
+      int ks = 0, count_s = z.count;
+      bool two_s = z.two;
+      // S of the turn that z is at, by group w
+      auto scores = [&](int w) {
+        if (!z.half) {  // (the tile's first)
+          if (z.i == 0) wait(&S.q_full, z.k);
+          wait(&S.k_full[z.f % KS], z.f / KS);
+        }
         if (!ok) return;
         tc_fence_after();
-        const uint64_t qd = sw128_desc(smem_u32(qbuf + q * C::TILE)), kd = sw128_desc(smem_u32(kring + fz % KS * C::TILE));
+        const uint64_t qd = sw128_desc(smem_u32(qbuf + (z.two ? w : 0) * C::TILE)), kd = sw128_desc(smem_u32(kring + z.f % KS * C::TILE));
 #pragma unroll
         for (int x = 0; x < DP / 16; ++x) {  // (addresses in a descriptor count 16 bytes)
           const uint32_t at = (x / 4 * (AT_KEYS * 128) + x % 4 * 32) / 16;
           mma_f16(tmem + w * 128, qd + at, kd + at, id_s, x > 0);
         }
         mma_commit(&S.s_full[w]);
-        ++jz;
-        half = two_z && !half;
-        if (half) return;
-        mma_commit(&S.k_empty[fz % KS]);
-        ++fz;
-        if (++iz == count_z) {
-          mma_commit(&S.q_empty);
-          segment(++kz, count_z, two_z);
-          iz = 0;
-        }
+        const int slot = z.f % KS, left = z.step(S.segs, tok, a.status);
+        if (left) mma_commit(&S.k_empty[slot]);
+        if (left == 2) mma_commit(&S.q_empty);
       };
-      for (int j = 0; ok && j < 2 && count_z; ++j) scores();
+      for (int j = 0; ok && j < 2 && z.count; ++j) scores(j);
       int f = 0, i = 0;
       bool half_v = false;
       for (int j = 0; ok && count_s; ++j) {
         const int w = j & 1;
         wait(&S.p_full[w], j >> 1);
-        wait(&S.v_ready[f % VS], f / VS);
         if (!ok) break;
         tc_fence_after();
         const uint64_t vd = sw128_mn_desc(smem_u32(vring + f % VS * C::TILE), AT_KEYS * 128);
@@ -296,23 +311,23 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         for (int x = 0; x < AT_KEYS / 16; ++x)
           mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + x * 8, vd + x * 2048 / 16, id_o, true);
         if (i + (two_s ? 1 : 2) >= count_s) mma_commit(&S.o_full[w]);  // the group's last turn of the segment
+        if (z.count) scores(w);
         half_v = two_s && !half_v;
-        bool over = false;
         if (!half_v) {
           mma_commit(&S.v_empty[f % VS]);
           ++f;
-          over = ++i == count_s;
-        }
-        if (count_z) scores();
-        if (over) {
-          mbar_arrive(&S.segs.empty[ks % AT_SEGS]);
-          segment(++ks, count_s, two_s);
-          i = 0;
+          if (++i == count_s) {
+            mbar_arrive(&S.segs.empty[ks % AT_SEGS]);
+            const Seg &g = S.segs.get(++ks, a.status);
+            count_s = g.count;
+            two_s = g.n > tok;
+            i = 0;
+          }
         }
       }
       while (count_s) {  // (gave up)
         mbar_arrive(&S.segs.empty[ks % AT_SEGS]);
-        segment(++ks, count_s, two_s);
+        count_s = S.segs.get(++ks, a.status).count;
       }
       mma_commit(&S.drain);
       int off = 0;
@@ -329,6 +344,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     int f = 0, turn = 0, mine = 0, ends = 0;  // tile and turn of the stretch; turns and segments of this group
     for (int ks = 0;; ++ks) {
       const Seg &s = S.segs.get(ks, a.status);
+      __syncwarp();
       const int count = s.count;
       if (!count) break;
       const bool two = s.n > tok;
@@ -348,7 +364,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       for (int i = 0; i < count; ++i, j0 += AT_KEYS, ++f) {
         turn += two ? 2 : 1;
         if (!two && ((turn - 1) & 1) != grp) continue;
-        at_wait(&S.s_full[grp], mine & 1, &S.gave_up, a.status);
+        at_wait_warp(&S.s_full[grp], mine & 1, &S.gave_up, a.status);
         tc_fence_after();
         // columns [lo, hi) of the tile are seen; the others' scores are
         // replaced in tensor memory (a short loop: the code of the common
@@ -365,15 +381,15 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
           }
           tmem_st_wait();
         }
-        float x[AT_KEYS];
-        tmem_ld64(t_s, x);
-        tmem_ld64(t_s + 64, x + 64);
-        float t0 = x[0], t1 = x[1], t2 = x[2], t3 = x[3];
+        float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
+#pragma unroll 1
+        for (int c0 = 0; c0 < AT_KEYS; c0 += 64) {
+          float x[64];
+          tmem_ld64(t_s + c0, x);
 #pragma unroll
-        for (int c = 4; c < AT_KEYS; c += 8) {
-          t0 = fmaxf(t0, fmaxf(x[c], x[c + 1]));
-          t1 = fmaxf(t1, fmaxf(x[c + 2], x[c + 3]));
-          if (c + 4 < AT_KEYS) {
+          for (int c = 0; c < 64; c += 8) {
+            t0 = fmaxf(t0, fmaxf(x[c], x[c + 1]));
+            t1 = fmaxf(t1, fmaxf(x[c + 2], x[c + 3]));
             t2 = fmaxf(t2, fmaxf(x[c + 4], x[c + 5]));
             t3 = fmaxf(t3, fmaxf(x[c + 6], x[c + 7]));
           }
@@ -398,16 +414,20 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         }
         const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll 1
+        for (int c0 = 0; c0 < AT_KEYS; c0 += 64) {
+          float x[64];
+          tmem_ld64(t_s + c0, x);
 #pragma unroll
-        for (int c = 0; c < AT_KEYS; c += 4) {
-          const float2 u = fma2(make_float2(x[c], x[c + 1]), sc2, m2), w = fma2(make_float2(x[c + 2], x[c + 3]), sc2, m2);
-          const float2 p = make_float2(ex2(u.x), ex2(u.y)), q = make_float2(ex2(w.x), ex2(w.y));
-          sum0 = add2(sum0, p);
-          sum1 = add2(sum1, q);
-          x[c / 2] = __uint_as_float(pack16<BF16>(p.x, p.y));
-          x[c / 2 + 1] = __uint_as_float(pack16<BF16>(q.x, q.y));
-          if (c == 60) tmem_st32(t_s, x);
-          if (c == 124) tmem_st32(t_s + 32, x + 32);
+          for (int c = 0; c < 64; c += 4) {
+            const float2 u = fma2(make_float2(x[c], x[c + 1]), sc2, m2), w = fma2(make_float2(x[c + 2], x[c + 3]), sc2, m2);
+            const float2 p = make_float2(ex2(u.x), ex2(u.y)), q = make_float2(ex2(w.x), ex2(w.y));
+            sum0 = add2(sum0, p);
+            sum1 = add2(sum1, q);
+            x[c / 2] = __uint_as_float(pack16<BF16>(p.x, p.y));
+            x[c / 2 + 1] = __uint_as_float(pack16<BF16>(q.x, q.y));
+          }
+          tmem_st32(t_s + c0 / 2, x);
         }
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
         if (edge_of(p0, n0, j0)) {
@@ -415,7 +435,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
           // probability of zero does not take them away, so the rows that see
           // them have them added here, and the products get zeros
           const int sl = f % VS;
-          at_wait(&S.v_seen[sl], f / VS & 1, &S.gave_up, a.status);
+          at_wait_warp(&S.v_seen[sl], f / VS & 1, &S.gave_up, a.status);
           if (S.odd[sl][0] | S.odd[sl][1] | S.odd[sl][2] | S.odd[sl][3]) {
             const uint8_t *vt = vring + sl * C::TILE;
             for (int k = 0; k < AT_KEYS; ++k) {
@@ -437,17 +457,19 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.added[grp]);
           }
+          __syncwarp();
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full[grp]);
+        __syncwarp();
         ++mine;
         ++done;
       }
       // ---- the segment's end ----
       if (done) {
-        at_wait(&S.o_full[grp], ends++ & 1, &S.gave_up, a.status);
+        at_wait_warp(&S.o_full[grp], ends++ & 1, &S.gave_up, a.status);
         tc_fence_after();
       }
       const bool whole = (s.flags & (SEG_START | SEG_END)) == (SEG_START | SEG_END);
@@ -458,7 +480,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       if (!two) {
         S.stats[grp][row] = make_float2(m, l);
         tc_fence_before();
-        named_bar(1, 256);
+        warps_bar(1, 256);
         tc_fence_after();
         const float2 o = S.stats[1 - grp][row];
         const float to = fmaxf(m, o.x);
@@ -476,6 +498,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       uint16_t *out = a.out + t * a.os + (int64_t)h * a.D;
       float *sums = pieces.sums + (piece * AC_ROWS + (two ? grp * 128 : 0) + row) * DP;
       for (int c = c0; c < c1; c += 16) {
+        __syncwarp();  // the loads are the whole warp's, the stores those of lanes with a row
         float o[16];
         tmem_ld16(t_o + c, o);
 #pragma unroll
@@ -486,23 +509,22 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = fmaf(p[k], other, o[k]);
         }
-        if (!is_row) continue;
-        if (!whole) {
+        if (is_row && !whole) {
 #pragma unroll
           for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4 *>(sums + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-          continue;
-        }
+        } else if (is_row) {
 #pragma unroll
-        for (int k = 0; k < 16; k += 8) {
-          if (wide_out) {  // (head_dim is a multiple of 8)
-            if (c + k < a.D)
-              *reinterpret_cast<uint4 *>(out + c + k) =
-                  make_uint4(pack16<BF16>(o[k], o[k + 1]), pack16<BF16>(o[k + 2], o[k + 3]),
-                             pack16<BF16>(o[k + 4], o[k + 5]), pack16<BF16>(o[k + 6], o[k + 7]));
-          } else {
+          for (int k = 0; k < 16; k += 8) {
+            if (wide_out) {  // (head_dim is a multiple of 8)
+              if (c + k < a.D)
+                *reinterpret_cast<uint4 *>(out + c + k) =
+                    make_uint4(pack16<BF16>(o[k], o[k + 1]), pack16<BF16>(o[k + 2], o[k + 3]),
+                               pack16<BF16>(o[k + 4], o[k + 5]), pack16<BF16>(o[k + 6], o[k + 7]));
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (c + k + e < a.D) out[c + k + e] = (uint16_t)pack16<BF16>(o[k + e], 0.f);
+              for (int e = 0; e < 8; ++e)
+                if (c + k + e < a.D) out[c + k + e] = (uint16_t)pack16<BF16>(o[k + e], 0.f);
+            }
           }
         }
       }
@@ -512,11 +534,13 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       }
       if (!whole && tid == 0)
         pieces.what[piece] = make_int4(s.r, s.h, s.b, PIECE_USED | (s.flags & SEG_START ? PIECE_START : 0) | (s.flags & SEG_END ? PIECE_END : 0));
+      __syncwarp();
       tc_fence_before();
       S.segs.done(ks);
-      if (!two) named_bar(1, 256);  // both have read both's sums
+      if (!two) warps_bar(1, 256);  // both have read both's sums
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == AC_MMA) {

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
   for (int i = tid; i < (int)(2 * C::Q / 16); i += AD_THREADS) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
   find_start<AD_THREADS>(a, TPB, &S.start, S.part);
+  __syncwarp();
   __syncthreads();
   if (warp == AD_MMA) tmem_alloc<C::TMEM>(&S.tmem);
   tc_fence_before();
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
       float l[N];
 #pragma unroll
       for (int c = 0; c < N; ++c) l[c] = 0.f;
+      __syncwarp();
       {
         const float z[16] = {};
 #pragma unroll
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
         tmem_st_wait();
       }
       if (key < N) S.ref[grp][key] = AT_NONE;
-      named_bar(1 + grp, 128);
+      warps_bar(1 + grp, 128);
       int done = 0;
       const int f_end = f + s.count;
       for (int i = 0; f < f_end; ++f, ++i) {
@@ -230,13 +232,13 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
         const int j0 = (s.tile + i) * AT_KEYS;
         const bool edge = j0 + AT_KEYS - 1 > pos0 || (a.window && j0 < pos0 + s.n - a.window);
         const uint32_t t_s = tmem + lanes + (f % AD_AHEAD) * N;
-        at_wait(&S.s_full[f % AD_AHEAD], (f / AD_AHEAD) & 1, &S.gave_up, a.status);
+        at_wait_warp(&S.s_full[f % AD_AHEAD], (f / AD_AHEAD) & 1, &S.gave_up, a.status);
         tc_fence_after();
         // the group's last products: their probabilities' room and the sums are free once they are complete
         bool settled = mine == 0;
         auto settle = [&]() {
           if (!settled) {
-            at_wait(&S.o_full[grp], (mine - 1) & 1, &S.gave_up, a.status);
+            at_wait_warp(&S.o_full[grp], (mine - 1) & 1, &S.gave_up, a.status);
             tc_fence_after();
           }
           settled = true;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           for (int c = 0; c < N; ++c) v[c] = isnan(v[c]) || (edge && (c < lo || c >= hi)) ? -INFINITY : v[c] * sc;
           const float t = warp_columns<N, true>(v);
           if (lane < N) S.top[grp][wq][lane] = t;
-          named_bar(1 + grp, 128);
+          warps_bar(1 + grp, 128);
           if (key < N) {
             const float was = S.ref[grp][key];
             const float to = fmaxf(fmaxf(fmaxf(S.top[grp][0][key], S.top[grp][1][key]),
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
             S.ref[grp][key] = to;
             S.factor[grp][key] = ex2(was - to);
           }
-          named_bar(1 + grp, 128);
+          warps_bar(1 + grp, 128);
           if (done) {
 #pragma unroll
             for (int c = 0; c < N; ++c) l[c] *= S.factor[grp][c];
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           // take away an infinity or NaN, so rows that no token sees are
           // cleared, and what is not finite in others is added to the sums of
           // the rows that see it, and cleared
-          at_wait(&S.full[1][f % SLOTS], (f / SLOTS) & 1, &S.gave_up, a.status);
+          at_wait_warp(&S.full[1][f % SLOTS], (f / SLOTS) & 1, &S.gave_up, a.status);
           uint8_t *vt = vring + f % SLOTS * C::TILE, *vr = vt + key * 128;
           bool odd = false;
           if (hi <= lo) {
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           if (s.n > 1 && bar_or(1 + grp, 128, odd)) {
             const uint32_t m = __ballot_sync(0xffffffffu, odd);
             if (lane == 0) S.odd[grp][wq] = m;
-            named_bar(1 + grp, 128);
+            warps_bar(1 + grp, 128);
             const int d = key & (DP - 1);
             for (int k = 0; k < AT_KEYS; ++k) {
               if (!(S.odd[grp][k >> 5] >> (k & 31) & 1u)) continue;
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
               }
               tmem_st_wait();
             }
-            named_bar(1 + grp, 128);
+            warps_bar(1 + grp, 128);
             if (odd) {
               for (int x = 0; x < DP / 2; ++x) {
                 uint32_t *w = reinterpret_cast<uint32_t *>(vr + x / 32 * (AT_KEYS * 128) + x % 32 * 4);
@@ -364,6 +366,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full[grp]);
+        __syncwarp();
         ++mine;
         ++done;
       }
@@ -373,12 +376,12 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
         if (lane < N) S.sum[grp][wq][lane] = t;
       }
       if (done) {
-        at_wait(&S.o_full[grp], (mine - 1) & 1, &S.gave_up, a.status);
+        at_wait_warp(&S.o_full[grp], (mine - 1) & 1, &S.gave_up, a.status);
         tc_fence_after();
       }
       // both groups' products are done before the probabilities' room is
       // taken for the exchange: [rows][DP] sums
-      named_bar(3, 256);
+      warps_bar(3, 256);
       float *ex = reinterpret_cast<float *>(pbuf);
       constexpr int HALF = N / 2;
       const bool whole = s.has_start() && s.has_end();
@@ -401,6 +404,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           pieces.stats[piece * N + row] = make_float2(m, total);
         }
       }
+      __syncwarp();
       float o[HALF];
 #pragma unroll
       for (int c = 0; c < HALF; c += 8) tmem_ld8(t_o + (1 - grp) * HALF + c, o + c);
@@ -408,10 +412,11 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
 #pragma unroll
         for (int c = 0; c < HALF; ++c) ex[((1 - grp) * HALF + c) * DP + key] = o[c];
       }
+      __syncwarp();
 #pragma unroll
       for (int c = 0; c < HALF; c += 8) tmem_ld8(t_o + grp * HALF + c, o + c);
       tc_fence_before();
-      named_bar(3, 256);
+      warps_bar(3, 256);
       if (key < (whole ? a.D : DP)) {
 #pragma unroll
         for (int c = 0; c < HALF; ++c) {
@@ -427,9 +432,10 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
       }
       if (!whole && tid == 0)
         pieces.what[piece] = make_int4(s.r, s.h, 0, PIECE_USED | (s.has_start() ? PIECE_START : 0) | (s.has_end() ? PIECE_END : 0));
-      named_bar(3, 256);
+      warps_bar(3, 256);
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == AD_MMA) {

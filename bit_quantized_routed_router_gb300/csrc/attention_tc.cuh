@@ -48,9 +48,23 @@ __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t par, int *gave_u
   return true;
 }
 
+// The same by a whole warp, which has to be together again for the collective
+// instructions that follow (tensor-memory loads and stores, barriers).
+__device__ __forceinline__ bool at_wait_warp(uint64_t *bar, uint32_t par, int *gave_up, unsigned *status) {
+  const bool ok = at_wait(bar, par, gave_up, status);
+  __syncwarp();
+  return ok;
+}
+
+__device__ __forceinline__ void warps_bar(int id, int count) {
+  __syncwarp();
+  named_bar(id, count);
+}
+
 // Whether any of the `count` threads at named barrier `id` says so.
 __device__ __forceinline__ bool bar_or(int id, int count, bool v) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %3, 0;\n\t"

@@ -90,6 +90,9 @@ CASES = {
     "shorter_than_chunk": ([0, 0], [5, 200], 4, 2, 128, 16, dict(seq=[3, 40])),
     "empty_sequence": ([0, 30], [5, 1], 4, 2, 128, 16, dict(seq=[0, 31])),
     "many_requests": (ref.lengths(R, 70, 0, 300), ref.lengths(R, 70, 0, 3), 8, 2, 64, 16, {}),
+    "many_chunks": (ref.lengths(R, 40, 0, 900), [9] * 40, 16, 2, 128, 64, {}),
+    "many_chunks_64": (ref.lengths(R, 60, 0, 300), ref.lengths(R, 60, 1, 40), 14, 2, 64, 16, dict(dtype="f16")),
+    "chunks_and_windows": (ref.lengths(R, 24, 0, 700), ref.lengths(R, 24, 1, 300), 2, 2, 64, 48, dict(window=200)),
     "sharp": ([700], [40], 4, 2, 128, 16, dict(qscale=12.0)),
     "sharp_decode": ([2000], [2], 4, 2, 128, 16, dict(qscale=12.0, dtype="f16")),
 }
