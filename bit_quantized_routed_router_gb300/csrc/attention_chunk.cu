@@ -22,9 +22,11 @@
 //   gate warp       in tiles that not every row sees it clears the values that
 //                   none sees and looks for infinities and NaN in the others;
 //                   and it waits for a turn's values in the MMA thread's
-//                   place, as one more arrival beside the probabilities': the
-//                   products stand still while the thread that issues them
-//                   waits (about 100 cycles for a barrier that is complete).
+//                   place and tells it what the turn is (a word of flags), as
+//                   one more arrival beside the probabilities': the products
+//                   stand still while the thread that issues them does
+//                   anything else, and a warp that runs alone takes hundreds
+//                   of cycles for a little bookkeeping.
 //
 // Maxima are raised lazily (AT_SLACK), by warp.
 #include "attention_tc.cuh"
@@ -34,7 +36,7 @@ namespace {
 
 constexpr int AC_THREADS = 384;
 constexpr int AC_MMA = 8, AC_KEYS = 9, AC_VALUES = 10, AC_GATE = 11;
-constexpr int AC_READERS = 11;  // warps that read the segments: all but the keys' producer
+constexpr int AC_READERS = 10;  // warps that read all segments: softmax, values, gate
 constexpr int AC_ROWS = 256;
 constexpr int AC_HEAD = 3 * 1024;  // bytes of a block's barriers and small arrays
 
@@ -42,6 +44,25 @@ template <int DP>
 struct AcCfg {
   static constexpr uint32_t TILE = AT_KEYS * DP * 2;  // keys, values, or a query tile
   static constexpr int KS = DP == 128 ? 2 : 4, VS = DP == 128 ? 3 : 4;
+};
+
+// What a turn is, for the MMA thread: its value slot, and of the scores that
+// follow (if any) the key slot and query tile, what to wait for, and what to
+// let go of behind them.
+enum : uint32_t {
+  TURN_SCORES = 1u << 0,   // the group has another turn
+  TURN_WAIT_K = 1u << 1,   // its keys are new
+  TURN_WAIT_Q = 1u << 2,   // its query rows are new
+  TURN_K_PAR = 1u << 3,
+  TURN_Q_PAR = 1u << 4,
+  TURN_Q_TILE = 1u << 5,
+  TURN_FREE_K = 1u << 6,
+  TURN_FREE_Q = 1u << 7,
+  TURN_FREE_V = 1u << 8,
+  TURN_SUMS = 1u << 9,     // the group's last of the segment
+  TURN_LAST = 1u << 10,    // the stretch's last
+  TURN_K_SLOT = 1u << 12,  // times the slot
+  TURN_V_SLOT = 1u << 16
 };
 
 template <int KS, int VS>
@@ -53,6 +74,7 @@ struct AcShared {
   uint32_t odd[VS][4];  // keys whose values are not all finite
   float2 stats[2][128]; // maximum and sum of a row, by group
   SegRing segs;
+  uint32_t turns[4];    // turn j's word at j mod 4
   int64_t part[AC_THREADS / 32];
   Start start;
   uint32_t tmem;
@@ -70,15 +92,22 @@ struct Ahead {
     two = g.n > tok;
     i = 0;
   }
-  // To the next turn; whether the tile's, and the segment's, last one was left.
-  __device__ __forceinline__ int step(SegRing &ring, int tok, unsigned *status) {
+  // The scores of the turn: their part of a word.
+  template <int KS>
+  __device__ __forceinline__ uint32_t word(int w) const {
     if (!count) return 0;
+    const bool last = two ? half : true;  // of the tile
+    return TURN_SCORES | (half ? 0u : TURN_WAIT_K | (f / KS & 1 ? TURN_K_PAR : 0u)) |
+           (!half && i == 0 ? TURN_WAIT_Q | (k & 1 ? TURN_Q_PAR : 0u) : 0u) | (two && w ? TURN_Q_TILE : 0u) |
+           (last ? TURN_FREE_K : 0u) | (last && i + 1 == count ? TURN_FREE_Q : 0u) | (uint32_t)(f % KS) * TURN_K_SLOT;
+  }
+  // To the next turn.
+  __device__ __forceinline__ void step(SegRing &ring, int tok, unsigned *status) {
+    if (!count) return;
     half = two && !half;
-    if (half) return 0;
+    if (half) return;
     ++f;
-    if (++i < count) return 1;
-    segment(ring, k + 1, tok, status);
-    return 2;
+    if (++i == count) segment(ring, k + 1, tok, status);
   }
 };
 
@@ -205,6 +234,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
   } else if (warp == AC_GATE) {
     // --------------------------------------------------------------- gate --
     int f = 0, turn = 0, adds[2] = {0, 0};
+    Ahead z{};
+    z.segment(S.segs, 0, tok, a.status);
+    for (int j = 0; j < 2; ++j) z.step(S.segs, tok, a.status);
     for (int k = 0;; ++k) {
       const Seg s = S.segs.get(k, a.status);
       if (!s.count) break;
@@ -261,78 +293,75 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         }
         for (int t = 0; t < (two ? 2 : 1); ++t) {
           const int j = turn + t, w = j & 1;
+          const bool tile_end = !two || t, sums = i + (two ? 1 : 2) >= s.count;
+          uint32_t word = z.word<KS>(w) | (uint32_t)sl * TURN_V_SLOT | (tile_end ? TURN_FREE_V : 0u) | (sums ? TURN_SUMS : 0u);
+          z.step(S.segs, tok, a.status);
+          // (the stretch's last turn has no other behind it: none after the
+          // next, and the segment after this one is its end)
+          if (tile_end && i + 1 == s.count && !S.segs.get(k + 1, a.status).count) word |= TURN_LAST;
           if (j >= 2) at_wait(&S.p_full[w], ((j >> 1) - 1) & 1, &S.gave_up, a.status);  // the arrival is for this turn
-          if (lane == 0) mbar_arrive(&S.p_full[w]);
+          if (lane == 0) {
+            S.turns[j & 3] = word;
+            mbar_arrive(&S.p_full[w]);
+          }
         }
       }
       S.segs.done(k);
     }
   } else if (warp == AC_MMA) {
     // ----------------------------------------------------------- products --
-    if (lane == 0) {
-      const uint32_t id_s = f16_idesc(AT_KEYS, BF16), id_o = f16_idesc(DP, BF16) | IDESC_B_MN;
-      bool ok = true;
-      auto wait = [&](uint64_t *b, int par) {
-        if (ok && !at_wait(b, par & 1, &S.gave_up, a.status)) ok = false;
-      };
-      Ahead z{};
-      z.segment(S.segs, 0, tok, a.status);
-      int ks = 0, count_s = z.count;
-      bool two_s = z.two;
-      // S of the turn that z is at, by group w
-      auto scores = [&](int w) {
-        if (!z.half) {  // (the tile's first)
-          if (z.i == 0) wait(&S.q_full, z.k);
-          wait(&S.k_full[z.f % KS], z.f / KS);
-        }
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t qd = sw128_desc(smem_u32(qbuf + (z.two ? w : 0) * C::TILE)), kd = sw128_desc(smem_u32(kring + z.f % KS * C::TILE));
+    // (the whole warp walks; one lane issues)
+    const uint32_t by = elect_one();
+    const uint32_t id_s = f16_idesc(AT_KEYS, BF16), id_o = f16_idesc(DP, BF16) | IDESC_B_MN;
+    const uint64_t q0 = sw128_desc(smem_u32(qbuf)), k0 = sw128_desc(smem_u32(kring));
+    const uint64_t v0 = sw128_mn_desc(smem_u32(vring), AT_KEYS * 128);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    bool ok = true;
+    auto wait = [&](uint64_t *b, uint32_t par) { ok = __all_sync(0xffffffffu, at_wait(b, par, &S.gave_up, a.status)) && ok; };
+    auto scores = [&](int w, uint32_t word) {
+      if (word & TURN_WAIT_Q) wait(&S.q_full, word & TURN_Q_PAR ? 1 : 0);
+      const int slot = word / TURN_K_SLOT & 15;
+      if (word & TURN_WAIT_K) wait(&S.k_full[slot], word & TURN_K_PAR ? 1 : 0);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t qd = q0 + (word & TURN_Q_TILE ? C::TILE / 16 : 0), kd = k0 + slot * (C::TILE / 16);
 #pragma unroll
-        for (int x = 0; x < DP / 16; ++x) {  // (addresses in a descriptor count 16 bytes)
-          const uint32_t at = (x / 4 * (AT_KEYS * 128) + x % 4 * 32) / 16;
-          mma_f16(tmem + w * 128, qd + at, kd + at, id_s, x > 0);
-        }
-        mma_commit(&S.s_full[w]);
-        const int slot = z.f % KS, left = z.step(S.segs, tok, a.status);
-        if (left) mma_commit(&S.k_empty[slot]);
-        if (left == 2) mma_commit(&S.q_empty);
-      };
-      for (int j = 0; ok && j < 2 && z.count; ++j) scores(j);
-      int f = 0, i = 0;
-      bool half_v = false;
-      for (int j = 0; ok && count_s; ++j) {
-        const int w = j & 1;
-        wait(&S.p_full[w], j >> 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t vd = sw128_mn_desc(smem_u32(vring + f % VS * C::TILE), AT_KEYS * 128);
-#pragma unroll
-        for (int x = 0; x < AT_KEYS / 16; ++x)
-          mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + x * 8, vd + x * 2048 / 16, id_o, true);
-        if (i + (two_s ? 1 : 2) >= count_s) mma_commit(&S.o_full[w]);  // the group's last turn of the segment
-        if (z.count) scores(w);
-        half_v = two_s && !half_v;
-        if (!half_v) {
-          mma_commit(&S.v_empty[f % VS]);
-          ++f;
-          if (++i == count_s) {
-            mbar_arrive(&S.segs.empty[ks % AT_SEGS]);
-            const Seg &g = S.segs.get(++ks, a.status);
-            count_s = g.count;
-            two_s = g.n > tok;
-            i = 0;
-          }
-        }
+      for (int x = 0; x < DP / 16; ++x) {  // (addresses in a descriptor count 16 bytes)
+        const uint32_t at = (x / 4 * (AT_KEYS * 128) + x % 4 * 32) / 16;
+        mma_f16_by(by, tm + w * 128, qd + at, kd + at, id_s, x > 0);
       }
-      while (count_s) {  // (gave up)
-        mbar_arrive(&S.segs.empty[ks % AT_SEGS]);
-        count_s = S.segs.get(++ks, a.status).count;
-      }
-      mma_commit(&S.drain);
-      int off = 0;
-      at_wait(&S.drain, 0, &off, a.status);
+      mma_commit_by(by, &S.s_full[w]);
+      if (word & TURN_FREE_K) mma_commit_by(by, &S.k_empty[slot]);
+      if (word & TURN_FREE_Q) mma_commit_by(by, &S.q_empty);
+    };
+    // the first turn's scores of each group, which no turn precedes (their
+    // segments are not let go of before these scores are used)
+    Ahead z{};
+    z.segment(S.segs, 0, tok, a.status);
+    const bool some = z.count > 0;
+    for (int j = 0; ok && j < 2 && z.count; ++j) {
+      scores(j, __shfl_sync(0xffffffffu, z.word<KS>(j), 0));
+      if (j == 0) z.step(S.segs, tok, a.status);
     }
+    for (int j = 0; ok && some; ++j) {
+      const int w = j & 1;
+      wait(&S.p_full[w], j >> 1 & 1);
+      if (!ok) break;
+      const uint32_t word = __shfl_sync(0xffffffffu, S.turns[j & 3], 0);
+      tc_fence_after();
+      const int slot = word / TURN_V_SLOT & 15;
+      const uint64_t vd = v0 + slot * (C::TILE / 16);
+#pragma unroll
+      for (int x = 0; x < AT_KEYS / 16; ++x)
+        mma_f16_ts_by(by, tm + 256 + w * 128, tm + w * 128 + x * 8, vd + x * 2048 / 16, id_o, true);
+      if (word & TURN_SUMS) mma_commit_by(by, &S.o_full[w]);
+      if (word & TURN_SCORES) scores(w, word);
+      if (word & TURN_FREE_V) mma_commit_by(by, &S.v_empty[slot]);
+      if (word & TURN_LAST) break;
+    }
+    mma_commit_by(by, &S.drain);
+    int off = 0;
+    at_wait(&S.drain, 0, &off, a.status);
     __syncwarp();
   } else {
     // ------------------------------------------------------------- softmax --

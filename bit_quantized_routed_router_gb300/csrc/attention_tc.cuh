@@ -33,9 +33,11 @@ constexpr float AT_LN2 = 0.69314718055994531f;
 constexpr float AT_SLACK = 8.f;
 constexpr float AT_NONE = -FLT_MAX;  // maximum of no scores
 
-// Bounded wait; once one has run out, every wait gives up at once.
-__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t par, int *gave_up, unsigned *status) {
-  if (mbar_try_wait(bar, par)) return true;
+// Bounded wait; once one has run out, every wait gives up at once.  (What
+// follows the first try is one function for the whole kernel: warps of
+// different roles share an instruction cache, and inlined at every wait it
+// would take most of it.)
+__device__ __noinline__ bool at_wait_long(uint64_t *bar, uint32_t par, int *gave_up, unsigned *status) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait_sleep(bar, par, 2000u)) {
     if (*(volatile int *)gave_up) return false;
@@ -46,6 +48,9 @@ __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t par, int *gave_u
     }
   }
   return true;
+}
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t par, int *gave_up, unsigned *status) {
+  return mbar_try_wait(bar, par) || at_wait_long(bar, par, gave_up, status);
 }
 
 // The same by a whole warp, which has to be together again for the collective
