@@ -259,11 +259,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
               for (int x = 0; x < DP / 8; ++x)
                 *reinterpret_cast<uint4 *>(vr + x / 8 * (AT_KEYS * 128) + x % 8 * 16) = make_uint4(0, 0, 0, 0);
             } else if (j >= all_hi || j < all_lo) {
-#pragma unroll
-              for (int x = 0; x < DP / 8; ++x) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(vr + x / 8 * (AT_KEYS * 128) + x % 8 * 16);
-                odd |= not_finite2<BF16>(w.x) || not_finite2<BF16>(w.y) || not_finite2<BF16>(w.z) || not_finite2<BF16>(w.w);
-              }
+              odd = not_finite_row<BF16, DP / 8>(vr);
             }
             m[k] = __ballot_sync(0xffffffffu, odd);
             any |= m[k];
@@ -396,25 +392,20 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         at_wait_warp(&S.s_full[grp], mine & 1, &S.gave_up, a.status);
         tc_fence_after();
         // columns [lo, hi) of the tile are seen; the others' scores are
-        // replaced in tensor memory (a short loop: the code of the common
-        // path has to stay in the instruction cache)
+        // replaced in tensor memory too
         const int hi = is_row ? pos + 1 - j0 : 0, lo = a.window ? pos + 1 - a.window - j0 : 0;
-        if (edge_of(p0 + skip, n, j0)) {
-#pragma unroll 1
-          for (int c = 0; c < AT_KEYS; c += 16) {
-            float v[16];
-            tmem_ld16(t_s + c, v);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = c + k >= lo && c + k < hi ? v[k] : -INFINITY;
-            tmem_st16(t_s + c, v);
-          }
-          tmem_st_wait();
-        }
+        const bool edge = edge_of(p0 + skip, n, j0);
         float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
 #pragma unroll 1
         for (int c0 = 0; c0 < AT_KEYS; c0 += 64) {
           float x[64];
           tmem_ld64(t_s + c0, x);
+          if (edge) {
+            const uint32_t s0 = bits(lo - c0, hi - c0), s1 = bits(lo - c0 - 32, hi - c0 - 32);
+#pragma unroll
+            for (int c = 0; c < 64; ++c) x[c] = (c < 32 ? s0 : s1) >> (c & 31) & 1u ? x[c] : -INFINITY;
+            tmem_st64(t_s + c0, x);
+          }
 #pragma unroll
           for (int c = 0; c < 64; c += 8) {
             t0 = fmaxf(t0, fmaxf(x[c], x[c + 1]));
@@ -423,6 +414,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             t3 = fmaxf(t3, fmaxf(x[c + 6], x[c + 7]));
           }
         }
+        if (edge) tmem_st_wait();
         const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sc;
         if (__any_sync(0xffffffffu, top > m + AT_SLACK)) {
           // raise the maximum, and bring the sums down to it (the earlier

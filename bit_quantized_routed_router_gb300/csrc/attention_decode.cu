@@ -325,11 +325,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
             for (int x = 0; x < DP / 8; ++x)
               *reinterpret_cast<uint4 *>(vr + x / 8 * (AT_KEYS * 128) + x % 8 * 16) = make_uint4(0, 0, 0, 0);
           } else if (lo > 0 || hi < nrows) {
-#pragma unroll
-            for (int x = 0; x < DP / 8; ++x) {
-              const uint4 w = *reinterpret_cast<const uint4 *>(vr + x / 8 * (AT_KEYS * 128) + x % 8 * 16);
-              odd |= not_finite2<BF16>(w.x) || not_finite2<BF16>(w.y) || not_finite2<BF16>(w.z) || not_finite2<BF16>(w.w);
-            }
+            odd = not_finite_row<BF16, DP / 8>(vr);
           }
           if (s.n > 1 && bar_or(1 + grp, 128, odd)) {
             const uint32_t m = __ballot_sync(0xffffffffu, odd);

@@ -151,6 +151,27 @@ __device__ __forceinline__ bool not_finite2(uint32_t w) {
 
 constexpr int AT_ITEM = 2;
 
+// Bits [lo, hi) of a word.
+__device__ __forceinline__ uint32_t bits(int lo, int hi) {
+  const uint32_t below = hi >= 32 ? 0xffffffffu : hi > 0 ? (1u << hi) - 1u : 0u;
+  return lo >= 32 ? 0u : lo > 0 ? below & ~((1u << lo) - 1u) : below;
+}
+
+// Whether any of a run of 16-byte words' 16-bit floats is an infinity or NaN:
+// the largest magnitude tells.
+template <bool BF16, int WORDS>
+__device__ __forceinline__ bool not_finite_row(const uint8_t *row) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int x = 0; x < WORDS; ++x) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(row + x / 8 * (AT_KEYS * 128) + x % 8 * 16);
+    top = __vimax3_u16x2(top, w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+    top = __vimax3_u16x2(top, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
+  }
+  constexpr uint32_t LEAST = BF16 ? 0x7F80u : 0x7C00u;
+  return (top & 0xffffu) >= LEAST || (top >> 16) >= LEAST;
+}
+
 // Tiles [begin, end) that tokens first .. first + n - 1 of a request see: one
 // at least, so that a block of tokens that sees no key is still written.
 __device__ __forceinline__ void tile_range(const Span &s, int first, int n, int window, int &begin, int &end) {
