@@ -145,55 +145,61 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
     }
   } else if (warp == AD_MMA) {
     // ----------------------------------------------------------- products --
-    if (lane == 0) {
-      const uint32_t idesc = f16_idesc(N, BF16);
-      Segments sk = s;
-      int ik = 0;  // tile of the segment that scores are at
-      bool ok = true;
-      auto scores = [&](int f) {
-        const int sl = f % SLOTS, b = sk.index & 1;
-        if (ik == 0 && !at_wait(&S.q_full[b], (sk.index >> 1) & 1, &S.gave_up, a.status)) ok = false;
-        if (!ok || !at_wait(&S.full[0][sl], (f / SLOTS) & 1, &S.gave_up, a.status)) { ok = false; return; }
-        tc_fence_after();
-        const uint64_t kd = sw128_desc(smem_u32(kring + sl * C::TILE)), qd = sw128_desc(smem_u32(qbuf + b * C::Q));
-        const uint32_t d = tmem + (f % AD_AHEAD) * N;
+    // (the whole warp walks; one lane issues)
+    const uint32_t by = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t idesc = f16_idesc(N, BF16);
+    const uint64_t k0 = sw128_desc(smem_u32(kring)), q0 = sw128_desc(smem_u32(qbuf)), p0 = sw128_desc(smem_u32(pbuf));
+    // head_dim 64: rows 64..127 of the second product repeat other elements and are not used
+    const uint64_t v0 = sw128_mn_desc(smem_u32(vring), DP == 128 ? AT_KEYS * 128 : 1024);
+    Segments sk = s;
+    int ik = 0;  // tile of the segment that scores are at
+    bool ok = true;
+    auto wait = [&](uint64_t *b, int par) { ok = __all_sync(0xffffffffu, at_wait(b, par & 1, &S.gave_up, a.status)) && ok; };
+    int kslot = 0, kpar = 0, vslot = 0, vpar = 0;
+    auto scores = [&](int f) {
+      const int b = sk.index & 1;
+      if (ik == 0) wait(&S.q_full[b], sk.index >> 1);
+      wait(&S.full[0][kslot], kpar);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t kd = k0 + kslot * (C::TILE / 16), qd = q0 + b * (C::Q / 16);
+      const uint32_t d = tm + (f % AD_AHEAD) * N;
 #pragma unroll
-        for (int x = 0; x < DP / 16; ++x)  // (addresses in a descriptor count 16 bytes)
-          mma_f16(d, kd + (x / 4 * (AT_KEYS * 128) + x % 4 * 32) / 16, qd + (x / 4 * (N * 128) + x % 4 * 32) / 16, idesc, x > 0);
-        mma_commit(&S.empty[0][sl]);
-        mma_commit(&S.s_full[f % AD_AHEAD]);
-        if (++ik == sk.count) {
-          mma_commit(&S.q_empty[b]);
-          sk.next(a, TPB);
-          ik = 0;
-        }
-      };
-      for (int f = 0; ok && f < AD_AHEAD && sk.count; ++f) scores(f);
-      int iv = 0;
-      for (int f = 0; ok && s.count; ++f) {
-        const int sl = f % SLOTS;
-        if (!at_wait(&S.p_full[f & 1], (f >> 1) & 1, &S.gave_up, a.status)) break;
-        if (!at_wait(&S.full[1][sl], (f / SLOTS) & 1, &S.gave_up, a.status)) break;
-        tc_fence_after();
-        // head_dim 64: rows 64..127 of the product repeat other elements and are not used
-        const uint64_t vd = sw128_mn_desc(smem_u32(vring + sl * C::TILE), DP == 128 ? AT_KEYS * 128 : 1024);
-        const uint64_t pd = sw128_desc(smem_u32(pbuf + (f & 1) * C::P));
-        const uint32_t d = tmem + (AD_AHEAD + (f & 1)) * N;
-#pragma unroll
-        for (int x = 0; x < AT_KEYS / 16; ++x)
-          mma_f16(d, vd + x * 2048 / 16, pd + (x / 4 * (N * 128) + x % 4 * 32) / 16, idesc | IDESC_A_MN, true);
-        mma_commit(&S.empty[1][sl]);
-        mma_commit(&S.o_full[f & 1]);
-        if (sk.count) scores(f + AD_AHEAD);
-        if (++iv == s.count) {
-          s.next(a, TPB);
-          iv = 0;
-        }
+      for (int x = 0; x < DP / 16; ++x)  // (addresses in a descriptor count 16 bytes)
+        mma_f16_by(by, d, kd + (x / 4 * (AT_KEYS * 128) + x % 4 * 32) / 16, qd + (x / 4 * (N * 128) + x % 4 * 32) / 16, idesc, x > 0);
+      mma_commit_by(by, &S.s_full[f % AD_AHEAD]);
+      mma_commit_by(by, &S.empty[0][kslot]);
+      if (++kslot == SLOTS) kslot = 0, kpar ^= 1;
+      if (++ik == sk.count) {
+        mma_commit_by(by, &S.q_empty[b]);
+        sk.next(a, TPB);
+        ik = 0;
       }
-      mma_commit(&S.drain);
-      int off = 0;
-      at_wait(&S.drain, 0, &off, a.status);
+    };
+    for (int f = 0; ok && f < AD_AHEAD && sk.count; ++f) scores(f);
+    int iv = 0;
+    for (int f = 0; ok && s.count; ++f) {
+      wait(&S.p_full[f & 1], f >> 1);
+      wait(&S.full[1][vslot], vpar);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t vd = v0 + vslot * (C::TILE / 16), pd = p0 + (f & 1) * (C::P / 16);
+      const uint32_t d = tm + (AD_AHEAD + (f & 1)) * N;
+#pragma unroll
+      for (int x = 0; x < AT_KEYS / 16; ++x)
+        mma_f16_by(by, d, vd + x * 2048 / 16, pd + (x / 4 * (N * 128) + x % 4 * 32) / 16, idesc | IDESC_A_MN, true);
+      mma_commit_by(by, &S.o_full[f & 1]);
+      mma_commit_by(by, &S.empty[1][vslot]);
+      if (++vslot == SLOTS) vslot = 0, vpar ^= 1;
+      if (sk.count) scores(f + AD_AHEAD);
+      if (++iv == s.count) {
+        s.next(a, TPB);
+        iv = 0;
+      }
     }
+    mma_commit_by(by, &S.drain);
+    int off = 0;
+    at_wait(&S.drain, 0, &off, a.status);
     __syncwarp();
   } else {
     // ------------------------------------------------------------- softmax --
