@@ -9,7 +9,7 @@ namespace dsm {
 namespace {
 
 constexpr int PM_THREADS = 512;
-constexpr int PM_MAX_REQUESTS = 16384;  // two ints a request in shared memory
+constexpr int PM_MAX_REQUESTS = 16384;  // three ints a request in shared memory
 constexpr int32_t MAX_LEN = 1 << 30;  // lengths are below it, so that two add up to an int
 
 // Exclusive scan of v over the block (PM_THREADS threads); total to all.
@@ -45,6 +45,19 @@ __device__ __forceinline__ int last_at_most(const int *a, int n, int v) {
   return lo;
 }
 
+// n / d for n < 2^31 and d <= 2^16 as a product and a shift: with 2^(s-1) < d
+// <= 2^s and m = ceil(2^(31+s) / d), floor(n m / 2^(31+s)) is the quotient
+// (Granlund and Montgomery, "Division by invariant integers", theorem 4.2).
+struct Divisor {
+  uint64_t m;
+  int shift;
+  explicit Divisor(uint32_t d) : shift(31) {
+    while (((uint64_t)1 << (shift - 31)) < d) ++shift;
+    m = (((uint64_t)1 << shift) + d - 1) / d;
+  }
+  __device__ __forceinline__ int of(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+
 struct PageMapArgs {
   const int32_t *context, *fresh;
   int R, page, n_free, width, cap;
@@ -54,68 +67,86 @@ struct PageMapArgs {
   int64_t *slots;
   int32_t *positions, *cu, *seq, *taken;
   unsigned *status;
+  Divisor by_page;
 };
 
 // Two exclusive scans over the requests (new tokens, then pages taken), which
-// every block makes for itself in shared memory, and then independent writes:
-// blocks share out the tokens and the new table entries.  The page of a token
-// that lies in a new page comes from the free list, not from the table, so no
-// block waits for another's entries.
+// every block makes for itself in shared memory, a thread PER requests, and
+// then independent writes: blocks share out the tokens and the new table
+// entries.  The page of a token that lies in a new page comes from the free
+// list, not from the table, so no block waits for another's entries.  Bound
+// by latency: the lengths' loads, the scans' barriers, a search per token.
+template <int PER>
 __global__ void __launch_bounds__(PM_THREADS) page_map_kernel(const PageMapArgs a) {
   extern __shared__ int sm[];
   int *cu = sm;              // [R + 1] first token of each request
-  int *base = sm + a.R + 1;  // [R + 1] first free-list index of each request
+  int *base = cu + a.R + 1;  // [R + 1] first free-list index of each request
+  int *ctx = base + a.R + 1; // [R] cached tokens
   __shared__ int64_t part[PM_THREADS / 32];
-  const int tid = threadIdx.x;
-  const int per = (a.R + PM_THREADS - 1) / PM_THREADS;
-  const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
+  const int tid = threadIdx.x, r0 = tid * PER;
   bool bad = false;
-  auto len = [&](const int32_t *p, int r) {
-    const int v = p[r];
+  auto valid = [&](int v) {
     if (v >= 0 && v < MAX_LEN) return v;
     bad = true;
     return 0;
   };
+  int c[PER], n[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const bool some = r0 + i < a.R;
+    c[i] = some ? a.context[r0 + i] : 0;
+    n[i] = some ? a.fresh[r0 + i] : 0;
+  }
   int64_t mine = 0, total;
-  for (int r = r0; r < r1; ++r) mine += len(a.fresh, r);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c[i] = valid(c[i]);
+    n[i] = valid(n[i]);
+    mine += n[i];
+  }
   int64_t run = block_scan(mine, part, total);
   if (total > a.cap) bad = true;
-  for (int r = r0; r < r1; ++r) {
-    cu[r] = (int)min(run, (int64_t)a.cap);
-    run += len(a.fresh, r);
+  mine = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int at = (int)min(run, (int64_t)a.cap);
+    run += n[i];
+    n[i] = (int)min(run, (int64_t)a.cap) - at;  // what there is room for
+    if (r0 + i < a.R) {
+      cu[r0 + i] = at;
+      ctx[r0 + i] = c[i];
+    }
   }
   if (tid == 0) cu[a.R] = (int)min(total, (int64_t)a.cap);
-  __syncthreads();
   // pages: held ones, and needed ones as far as the table goes
-  auto held_of = [&](int r) { return (int)min(((int64_t)len(a.context, r) + a.page - 1) / a.page, (int64_t)a.width); };
-  auto need_of = [&](int r) {
-    const int64_t n = ((int64_t)len(a.context, r) + (cu[r + 1] - cu[r]) + a.page - 1) / a.page;
-    if (n > a.width) bad = true;
-    return (int)min(n, (int64_t)a.width);
-  };
-  mine = 0;
-  for (int r = r0; r < r1; ++r) mine += need_of(r) - held_of(r);
-  run = block_scan(mine, part, total);
-  if (total > a.n_free) bad = true;
-  for (int r = r0; r < r1; ++r) {
-    base[r] = (int)run;
-    run += need_of(r) - held_of(r);
+  int take[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int held = min(a.by_page.of(c[i] + a.page - 1), a.width), need = a.by_page.of(c[i] + n[i] + a.page - 1);
+    if (need > a.width) bad = true;
+    take[i] = min(need, a.width) - held;
+    mine += take[i];
   }
-  if (tid == 0) base[a.R] = (int)total;
+  int64_t pages;
+  run = block_scan(mine, part, pages);
+  if (pages > a.n_free) bad = true;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (r0 + i < a.R) base[r0 + i] = (int)run;
+    run += take[i];
+  }
+  if (tid == 0) base[a.R] = (int)pages;
   __syncthreads();
   const int step = gridDim.x * PM_THREADS, first = blockIdx.x * PM_THREADS + tid;
   for (int r = first; r < a.R; r += step) {
     a.cu[r] = cu[r];
-    a.seq[r] = len(a.context, r) + (cu[r + 1] - cu[r]);
+    a.seq[r] = ctx[r] + (cu[r + 1] - cu[r]);
   }
   if (first == 0) {
     a.cu[a.R] = cu[a.R];
-    a.taken[0] = (int)min(total, (int64_t)a.n_free);
+    a.taken[0] = (int)min(pages, (int64_t)a.n_free);
   }
-  for (int p = first; p < base[a.R]; p += step) {
-    const int r = last_at_most(base, a.R, p);
-    a.table[r * a.table_stride + held_of(r) + p - base[r]] = p < a.n_free ? a.free_pages[p] : -1;
-  }
+  auto held_of = [&](int r) { return min(a.by_page.of(ctx[r] + a.page - 1), a.width); };
   for (int t = first; t < a.cap; t += step) {
     if (t >= cu[a.R]) {
       a.slots[t] = -1;
@@ -123,8 +154,8 @@ __global__ void __launch_bounds__(PM_THREADS) page_map_kernel(const PageMapArgs 
       continue;
     }
     const int r = last_at_most(cu, a.R, t);
-    const int pos = len(a.context, r) + t - cu[r];
-    const int col = pos / a.page, held = held_of(r);
+    const int pos = ctx[r] + t - cu[r];
+    const int col = a.by_page.of(pos), held = held_of(r);
     int page = -1;
     if (col < a.width) {
       if (col < held) {
@@ -135,10 +166,27 @@ __global__ void __launch_bounds__(PM_THREADS) page_map_kernel(const PageMapArgs 
       }
     }
     if (page < 0) bad = true;
-    a.slots[t] = page < 0 ? -1 : (int64_t)page * a.page + pos % a.page;
+    a.slots[t] = page < 0 ? -1 : (int64_t)page * a.page + (pos - col * a.page);
     a.positions[t] = pos;
   }
+  for (int p = first; p < base[a.R]; p += step) {
+    const int r = last_at_most(base, a.R, p);
+    a.table[r * a.table_stride + held_of(r) + p - base[r]] = p < a.n_free ? a.free_pages[p] : -1;
+  }
   if (bad) flag(a.status, ST_PAGING);
+}
+
+template <int PER>
+cudaError_t launch_page_map(const PageMapArgs &a, int sms, cudaStream_t s) {
+  static OncePerDevice once;
+  const cudaError_t e = once_per_device(once, []() {
+    return cudaFuncSetAttribute(page_map_kernel<PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(int) * (3 * PER * PM_THREADS + 2));
+  });
+  if (e != cudaSuccess) return e;
+  const int blocks = std::max(1, std::min(sms, (std::max(a.cap, a.R) + PM_THREADS - 1) / PM_THREADS));
+  page_map_kernel<PER><<<blocks, PM_THREADS, sizeof(int) * (3 * a.R + 2), s>>>(a);
+  return cudaGetLastError();
 }
 
 struct AppendArgs {
@@ -202,18 +250,13 @@ int ds_moe_page_map(const int32_t *context_lens, const int32_t *new_lens, int32_
       !aligned(n_taken, 4))
     return fail(err, errlen, DS_ERR_INVALID_ARG, "arrays must be aligned to their elements");
   PageMapArgs a{context_lens, new_lens, n_requests, page_size, n_free, table_width, max_tokens, free_pages, block_table,
-                table_stride, slots, positions, cu_new, seq_lens, n_taken, status_word()};
+                table_stride, slots, positions, cu_new, seq_lens, n_taken, status_word(), Divisor((uint32_t)page_size)};
   const int sms = device_sms();
   if (!a.status || !sms) return fail(err, errlen, DS_ERR_CUDA, "no CUDA device");
-  static OncePerDevice once;
-  cudaError_t e = once_per_device(once, []() {
-    return cudaFuncSetAttribute(page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sizeof(int) * 2 * (PM_MAX_REQUESTS + 1));
-  });
-  if (e != cudaSuccess) return cuda_fail(err, errlen, e, "page map set-up");
-  const int blocks = std::max(1, std::min(sms, (std::max(max_tokens, n_requests) + PM_THREADS - 1) / PM_THREADS));
-  page_map_kernel<<<blocks, PM_THREADS, sizeof(int) * 2 * (n_requests + 1), (cudaStream_t)stream>>>(a);
-  e = cudaGetLastError();
+  const cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = n_requests <= PM_THREADS       ? launch_page_map<1>(a, sms, s)
+                        : n_requests <= 4 * PM_THREADS ? launch_page_map<4>(a, sms, s)
+                                                       : launch_page_map<PM_MAX_REQUESTS / PM_THREADS>(a, sms, s);
   return e == cudaSuccess ? DS_OK : cuda_fail(err, errlen, e, "page map");
 }
 

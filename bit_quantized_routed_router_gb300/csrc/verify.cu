@@ -5,6 +5,8 @@
 // probability min(1, p(x) / q(x)), and at the first refusal a token is drawn
 // from max(p - q, 0), normalised; the tokens kept are then distributed as p's
 // own (speculative sampling, Leviathan et al. 2023, Chen et al. 2023).
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "errors.h"
 #include "internal.h"
@@ -13,8 +15,12 @@
 namespace dsm {
 namespace {
 
-constexpr int VD_THREADS = 1024;
-constexpr int VD_CHUNK = 1024;            // vocabulary entries a chunk sum covers
+namespace cg = cooperative_groups;
+
+constexpr int VD_THREADS = 256, VD_WARPS = VD_THREADS / 32;
+constexpr int VD_CLUSTER = 8;             // blocks a request at most
+constexpr int VD_RESIDENT = 4;            // blocks that an SM holds (64 registers a thread)
+constexpr int VD_CHUNK = 256;             // vocabulary entries a chunk sum covers
 constexpr int VD_MAX_VOCAB = 1 << 22;
 
 struct VerifyArgs {
@@ -29,41 +35,71 @@ struct VerifyArgs {
 
 template <bool BF16>
 __device__ __forceinline__ float prob(const void *base, int64_t i) {
-  return BF16 ? bf16_to_f32(((const uint16_t *)base)[i]) : ((const float *)base)[i];
+  return BF16 ? bf16_to_f32(__ldg((const uint16_t *)base + i)) : __ldg((const float *)base + i);
 }
 
 // What sampling takes a probability for: NaN and negative ones for 0, those
-// above 1 for 1 (reported).
+// above 1 for 1 (reported).  Others are what they are: their bits, as unsigned
+// words, are those of 1 at most (-0 is handled with the rest, and not
+// reported).
+constexpr uint32_t ONE_BITS = 0x3F800000u;
 __device__ __forceinline__ float clean(float p, bool &bad) {
-  if (p >= 0.f && p <= 1.f) return p;
+  if (p >= 0.f && p <= 1.f) return fabsf(p);
   bad = true;
   return p > 1.f ? 1.f : 0.f;
 }
 
-// max(p - q, 0) as a whole number of 2^-44 units, hi * 2^22 + lo with
-// hi <= 2^22 and |lo| <= 2^21 + 1.  The difference is held as a rounded sum
-// and its exact error (Knuth's two-sum); adding 1.5 * 2^23 rounds to whole
-// numbers.  Sums of such numbers are exact, so no order of adding changes
-// the token that is drawn; fp64 adds would be slower than HBM here.
-__device__ __forceinline__ void residual(float p, float q, int &hi, int &lo) {
-  const float MAGIC = 12582912.f, UNIT = 4194304.f;  // 1.5 * 2^23, 2^22
-  const float s = p - q, b = s - p, e = (p - (s - b)) + (-q - b);
-  const float t = fmaf(s, UNIT, MAGIC), h = t - MAGIC;
-  const float rem = fmaf(s, UNIT, -h) + e * UNIT;
-  const float u = fmaf(rem, UNIT, MAGIC);
-  const bool some = s > 0.f;
-  hi = some ? __float_as_int(t) - __float_as_int(MAGIC) : 0;
-  lo = some ? __float_as_int(u) - __float_as_int(MAGIC) : 0;
-}
-
-// Weight of entry x of a row that is sampled from: the target's, less the
-// draft's when q is given, or less all of it at the draft `sure`.
-template <bool BF16>
-__device__ __forceinline__ void weight(const void *p, int64_t prow, const void *q, int64_t qrow, int sure, int x, int &hi,
-                                       int &lo, bool &bad) {
-  const float pv = clean(prob<BF16>(p, prow + x), bad);
-  const float qv = q ? clean(prob<BF16>(q, qrow + x), bad) : (x == sure ? 1.f : 0.f);
-  residual(pv, qv, hi, lo);
+// Weights of 8 entries x0, x0 + step, ... of a row that is sampled from:
+// max(p - q, 0) with the target's p and the draft's q when q is given, or the
+// target's alone, but none at the draft `sure`.  All loads are under way
+// before the first is used; ALL: every entry is in the vocabulary.
+//
+// A weight is a whole number of 2^-44 units, hi * 2^22 + lo.  With q held to
+// at most p the difference is s plus an exact error e (Dekker's fast two-sum);
+// adding 1.5 * 2^23 rounds to whole numbers, which are the low bits of the
+// sum.  Sums of such numbers are exact, so no order of adding changes the
+// token that is drawn; fp64 adds would be slower than HBM here.
+template <bool BF16, bool ALL>
+__device__ __forceinline__ int64_t weights(const void *p, int64_t prow, const void *q, int64_t qrow, int sure, int x0, int step,
+                                           int V, int64_t each[8], bool &bad) {
+  constexpr float MAGIC = 12582912.f, UNIT = 4194304.f;  // 1.5 * 2^23, 2^22
+  constexpr uint32_t MAGIC_BITS = 0x4B400000u;
+  float pv[8], qv[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) pv[i] = ALL || x0 + i * step < V ? prob<BF16>(p, prow + x0 + i * step) : 0.f;
+  if (q) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) qv[i] = ALL || x0 + i * step < V ? prob<BF16>(q, qrow + x0 + i * step) : 0.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) qv[i] = 0.f;
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, max(__float_as_uint(pv[i]), __float_as_uint(qv[i])));
+  if (top > ONE_BITS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      pv[i] = clean(pv[i], bad);
+      qv[i] = clean(qv[i], bad);
+    }
+  }
+  if (sure >= 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pv[i] = x0 + i * step == sure ? 0.f : pv[i];
+  }
+  uint32_t hs = 0, ls = 0;  // (modulo 2^32)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = fminf(pv[i], qv[i]), s = pv[i] - y, e = (pv[i] - s) - y;
+    const float t = fmaf(s, UNIT, MAGIC);
+    const float rem = fmaf(e, UNIT, fmaf(s, UNIT, -(t - MAGIC)));
+    const uint32_t hi = __float_as_uint(t) - MAGIC_BITS, lo = __float_as_uint(fmaf(rem, UNIT, MAGIC)) - MAGIC_BITS;
+    if (each) each[i] = ((int64_t)(int)hi << 22) + (int)lo;
+    hs += hi;
+    ls += lo;
+  }
+  return ((int64_t)(int)hs << 22) + (int)ls;
 }
 
 __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
@@ -72,128 +108,140 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
   return v;
 }
 
-// One block a request.  Pass 1 sums the row chunk by chunk (a warp a chunk);
-// pass 2 finds the chunk that the drawn number falls into and the entry in it.
+// Sum over the earlier lanes and this one.
+__device__ __forceinline__ int64_t warp_scan64(int64_t v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v += w;
+  }
+  return v;
+}
+
+// A cluster of blocks a request, each with a part of the vocabulary: pass 1
+// sums the row chunk by chunk (a warp a chunk), the blocks exchange their
+// totals through shared memory, and the block that the drawn number falls
+// into finds the chunk and the entry in it.  Bound by reading one row of the
+// target and one of the draft.
 template <bool BF16>
-__global__ void __launch_bounds__(VD_THREADS) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const VerifyArgs a) {
   extern __shared__ int64_t chunk[];
-  __shared__ int s_kept, s_sure;
-  __shared__ int64_t s_total;
-  const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ int64_t totals[2][VD_CLUSTER], part[VD_WARPS];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+  const int r = blockIdx.x / ranks, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c0 = a.cu[r], c1 = a.cu[r + 1];
-  const int t0 = min(max(c0, 0), a.T), n_all = min(max(c1, t0), a.T) - t0, n = min(n_all, a.max_new);
+  const int t0 = min(max(c0, 0), a.T), n = min(min(max(c1, t0), a.T) - t0, a.max_new);
   bool bad = c0 != t0 || c1 != t0 + n;
   int32_t *out = a.out + (int64_t)r * a.max_new;
-  if (tid == 0) {
-    int kept = 0, sure = -1;
-    for (; kept < n - 1; ++kept) {
-      const int row = t0 + kept, x = a.tokens[row + 1];
-      if (x < 0 || x >= a.V) {
-        bad = true;
-        break;
-      }
-      const float pv = prob<BF16>(a.p, (int64_t)row * a.p_stride + x);
-      const float qv = a.q ? prob<BF16>(a.q, (int64_t)row * a.q_stride + x) : 1.f;
-      // products of two fp32 numbers are exact in fp64
-      if (!((double)a.u_accept[row] * (double)qv < (double)pv)) {
-        sure = x;
-        break;
+  // every warp counts the drafts that are kept: a lane a draft
+  int kept = 0, sure = -1;
+  for (; kept < n - 1;) {
+    const int row = t0 + kept + lane;
+    int x = -1;
+    bool keep = false;
+    if (kept + lane < n - 1) {
+      x = a.tokens[row + 1];
+      if (x >= 0 && x < a.V) {
+        const float pv = prob<BF16>(a.p, (int64_t)row * a.p_stride + x);
+        const float qv = a.q ? prob<BF16>(a.q, (int64_t)row * a.q_stride + x) : 1.f;
+        keep = (double)a.u_accept[row] * (double)qv < (double)pv;  // (products of two fp32 numbers are exact in fp64)
       }
     }
-    s_kept = kept;
-    s_sure = sure;
-    a.n_accepted[r] = kept;
+    const unsigned refuse = __ballot_sync(0xffffffffu, !keep);
+    if (refuse) {
+      const int f = __ffs(refuse) - 1;
+      kept += f;
+      x = __shfl_sync(0xffffffffu, x, f);
+      if (kept < n - 1) {
+        if (x >= 0 && x < a.V) sure = x;
+        else bad = true;
+      }
+      break;
+    }
+    kept += 32;
   }
-  __syncthreads();
-  const int kept = s_kept;
   const bool refused = kept < n - 1;
-  for (int i = tid; i < a.max_new; i += VD_THREADS)
-    if (i != kept || n == 0) out[i] = i < kept ? a.tokens[t0 + i + 1] : -1;
+  if (rank == 0) {
+    if (tid == 0) a.n_accepted[r] = max(kept, 0);
+    for (int i = tid; i < a.max_new; i += VD_THREADS)
+      if (i != kept || n == 0) out[i] = i < kept ? a.tokens[t0 + i + 1] : -1;
+  }
   if (n > 0) {
     const int64_t prow = (int64_t)(t0 + kept) * a.p_stride, qrow = (int64_t)(t0 + kept) * a.q_stride;
     const void *q = refused ? a.q : nullptr;
-    int sure = refused ? s_sure : -1;
-    const int chunks = (a.V + VD_CHUNK - 1) / VD_CHUNK;
-    int64_t total = 0;
+    if (!refused || q) sure = -1;
+    const int chunks = (a.V + VD_CHUNK - 1) / VD_CHUNK, per = (chunks + ranks - 1) / ranks;
+    const int first = min(chunks, rank * per), mine = min(chunks, first + per) - first;
+    int64_t total = 0, before = 0, own = 0;
     for (int turn = 0; turn < 2; ++turn) {
-      for (int c = warp; c < chunks; c += VD_THREADS / 32) {
-        int hs = 0, ls = 0;
-        for (int x = c * VD_CHUNK + lane; x < min(a.V, (c + 1) * VD_CHUNK); x += 32) {
-          int hi, lo;
-          weight<BF16>(a.p, prow, q, qrow, sure, x, hi, lo, bad);
-          hs += hi;
-          ls += lo;
-        }
-        const int64_t sum = warp_sum64(((int64_t)hs << 22) + ls);
-        if (lane == 0) chunk[c] = sum;
+      int64_t sum = 0;
+      for (int c = warp; c < mine; c += VD_WARPS) {
+        const int x0 = (first + c) * VD_CHUNK + lane;
+        const int64_t s = warp_sum64((first + c + 1) * VD_CHUNK <= a.V
+                                         ? weights<BF16, true>(a.p, prow, q, qrow, sure, x0, 32, a.V, nullptr, bad)
+                                         : weights<BF16, false>(a.p, prow, q, qrow, sure, x0, 32, a.V, nullptr, bad));
+        if (lane == 0) chunk[c] = s;
+        sum += s;
       }
+      if (lane == 0) part[warp] = sum;
       __syncthreads();
-      if (warp == 0) {
-        int64_t v = 0;
-        for (int c = lane; c < chunks; c += 32) v += chunk[c];
-        v = warp_sum64(v);
-        if (lane == 0) s_total = v;
+      if (tid < ranks) {  // this block's total to every block
+        int64_t s = 0;
+#pragma unroll
+        for (int w = 0; w < VD_WARPS; ++w) s += part[w];
+        *cluster.map_shared_rank(&totals[turn][rank], tid) = s;
       }
-      __syncthreads();
-      total = s_total;
+      cluster.sync();
+      total = before = 0;
+#pragma unroll
+      for (int i = 0; i < VD_CLUSTER; ++i) {
+        if (i >= ranks) break;
+        if (i < rank) before += totals[turn][i];
+        total += totals[turn][i];
+      }
+      own = totals[turn][rank];
       if (total > 0 || (!q && sure < 0)) break;
       q = nullptr;  // nothing left above the draft: the target itself
       sure = -1;
     }
     if (total <= 0) {
       bad = true;
-      if (tid == 0) out[kept] = -1;
+      if (rank == 0 && tid == 0) out[kept] = -1;
     } else if (warp == 0) {
       // the entry drawn is the least whose cumulative weight exceeds u * total
       const float u = a.u_sample[r];
       if (!(u >= 0.f && u < 1.f)) bad = true;
       int64_t thr = u >= 1.f ? total - 1 : u >= 0.f ? (int64_t)((double)u * (double)total) : 0;
       thr = min(thr, total - 1);
-      // thr is less than the total, so some chunk passes it
-      int64_t before = 0;
-      int at = 0;
-      for (int b = 0; b < chunks; b += 32) {
-        int64_t v = b + lane < chunks ? chunk[b + lane] : 0, incl = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t w = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += w;
-        }
-        const unsigned pass = __ballot_sync(0xffffffffu, before + incl > thr);
-        if (pass) {
-          const int f = __ffs(pass) - 1;
-          at = b + f;
-          before += __shfl_sync(0xffffffffu, incl - v, f);
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, incl, 31);
-      }
-      // each lane takes 32 entries in a row of that chunk
-      const int x0 = at * VD_CHUNK + lane * 32;
-      int64_t v = 0;
-      bool none = false;
-      for (int x = x0; x < min(a.V, x0 + 32); ++x) {
-        int hi, lo;
-        weight<BF16>(a.p, prow, q, qrow, sure, x, hi, lo, none);
-        v += ((int64_t)hi << 22) + lo;
-      }
-      int64_t incl = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t w = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += w;
-      }
-      const unsigned pass = __ballot_sync(0xffffffffu, before + incl > thr);
-      if (pass && lane == __ffs(pass) - 1) {
-        int64_t run = before + incl - v;
-        for (int x = x0; x < min(a.V, x0 + 32); ++x) {
-          int hi, lo;
-          weight<BF16>(a.p, prow, q, qrow, sure, x, hi, lo, none);
-          run += ((int64_t)hi << 22) + lo;
-          if (run > thr) {
-            out[kept] = x;
+      if (before <= thr && thr < before + own) {  // it is in this block's entries
+        int at = 0;
+        for (int b = 0; b < mine; b += 32) {
+          const int64_t v = b + lane < mine ? chunk[b + lane] : 0, incl = warp_scan64(v);
+          const unsigned pass = __ballot_sync(0xffffffffu, before + incl > thr);
+          if (pass) {
+            const int f = __ffs(pass) - 1;
+            at = b + f;
+            before += __shfl_sync(0xffffffffu, incl - v, f);
             break;
           }
+          before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        // each lane takes 8 entries in a row of that chunk
+        const int x0 = (first + at) * VD_CHUNK + lane * 8;
+        bool none = false;
+        int64_t each[8];
+        const int64_t v = weights<BF16, false>(a.p, prow, q, qrow, sure, x0, 1, a.V, each, none), incl = warp_scan64(v);
+        const unsigned pass = __ballot_sync(0xffffffffu, before + incl > thr);
+        if (pass && lane == __ffs(pass) - 1) {
+          int64_t run = before + incl - v;
+          int x = x0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (run <= thr) x = x0 + i;
+            run += each[i];
+          }
+          out[kept] = x;
         }
       }
     }
@@ -217,8 +265,8 @@ int ds_moe_verify_drafts(const void *target, int64_t target_stride, const void *
   if (vocab < 1 || vocab > VD_MAX_VOCAB)
     return fail(err, errlen, DS_ERR_INVALID_ARG, "vocab=%d: need 1..%d", vocab, VD_MAX_VOCAB);
   if (T < 0 || T > (1 << 24)) return fail(err, errlen, DS_ERR_INVALID_ARG, "T=%lld out of range", (long long)T);
-  if (n_requests < 0 || max_new < 0)
-    return fail(err, errlen, DS_ERR_INVALID_ARG, "negative n_requests or max_new");
+  if (n_requests < 0 || n_requests > (1 << 24) || max_new < 0)
+    return fail(err, errlen, DS_ERR_INVALID_ARG, "n_requests or max_new out of range");
   if (n_requests == 0) return DS_OK;
   if (max_new == 0) return fail(err, errlen, DS_ERR_INVALID_ARG, "max_new must be at least 1");
   if (T && (!target || !tokens || !u_accept))
@@ -234,12 +282,32 @@ int ds_moe_verify_drafts(const void *target, int64_t target_stride, const void *
   VerifyArgs a{target, draft, target_stride, draft_stride, (int)T, vocab, n_requests, max_new, tokens, cu_new, u_accept,
                u_sample, out_tokens, n_accepted, status_word()};
   if (!a.status) return fail(err, errlen, DS_ERR_CUDA, "no CUDA device");
-  const size_t smem = sizeof(int64_t) * ((vocab + VD_CHUNK - 1) / VD_CHUNK);
-  if (dtype == DS_F32)
-    verify_kernel<false><<<(unsigned)n_requests, VD_THREADS, smem, (cudaStream_t)stream>>>(a);
-  else
-    verify_kernel<true><<<(unsigned)n_requests, VD_THREADS, smem, (cudaStream_t)stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const int chunks = (vocab + VD_CHUNK - 1) / VD_CHUNK, sms = device_sms();
+  if (!sms) return fail(err, errlen, DS_ERR_CUDA, "no CUDA device");
+  // as many blocks a request as one wave of blocks has room for (96 requests
+  // of 100,003 entries: 27 us with 8, in two waves, 19 us with 4), and no more
+  // than there are chunks for their warps
+  int ranks = VD_CLUSTER;
+  while (ranks > 1 && ((int64_t)n_requests * ranks > sms * VD_RESIDENT || chunks <= VD_WARPS * (ranks / 2))) ranks /= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)n_requests * ranks);
+  cfg.blockDim = dim3(VD_THREADS);
+  cfg.dynamicSmemBytes = sizeof(int64_t) * ((chunks + ranks - 1) / ranks);
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ranks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  static OncePerDevice once;  // (the largest vocabulary's sums, in one block)
+  cudaError_t e = once_per_device(once, []() {
+    const int most = (int)sizeof(int64_t) * (VD_MAX_VOCAB / VD_CHUNK);
+    const cudaError_t f = cudaFuncSetAttribute(verify_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return f != cudaSuccess ? f : cudaFuncSetAttribute(verify_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  });
+  if (e == cudaSuccess)
+    e = dtype == DS_F32 ? cudaLaunchKernelEx(&cfg, verify_kernel<false>, a) : cudaLaunchKernelEx(&cfg, verify_kernel<true>, a);
   return e == cudaSuccess ? DS_OK : cuda_fail(err, errlen, e, "verify drafts");
 }
 
