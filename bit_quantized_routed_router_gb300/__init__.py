@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -171,8 +172,14 @@ def load(path: str):
     return L
 
 
+_tls = threading.local()
+
+
 def _call(fn, *args):
-    err = ctypes.create_string_buffer(512)
+    try:
+        err = _tls.err
+    except AttributeError:  # a message buffer for each thread
+        err = _tls.err = ctypes.create_string_buffer(512)
     rc = fn(*args, err, 512)
     if rc != DS_OK:
         raise DsMoeError(rc, err.value.decode(errors="replace"))
@@ -185,8 +192,16 @@ def _ptr(t):
 def _stream(stream):
     if stream is not None:
         return stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (no stream object is made for its address)
+        _current_stream = ((lambda: raw(torch.cuda.current_device())) if raw
+                           else (lambda: torch.cuda.current_stream().cuda_stream))
+    return _current_stream()
+
+
+_current_stream = None
 
 
 @dataclass
@@ -441,35 +456,49 @@ class KVCache:
             raise ValueError("k and v: [pages][page rows][heads][head_dim] of the same strides, the last axis dense")
         if k.element_size() != 2 or k.dtype != v.dtype or not (k.is_cuda and v.is_cuda):
             raise ValueError("k and v: 16-bit elements of one type on the device")
-        self.k, self.v, self.rows, self.heads, self.dim = k, v, k.shape[1], k.shape[2], k.shape[3]
+        self.k, self.v = k, v
+        self._geometry = (k.size(1), k.size(2), k.size(3))
         c = KVCacheC(k.data_ptr(), v.data_ptr(), k.shape[0], k.stride(0), k.stride(1), k.stride(2))
         self._c = ctypes.byref(c)
 
     def _fits(self, shape: AttentionShape):
-        if self.rows != shape.page_size or self.heads != shape.n_head_kv or self.dim != shape.head_dim:
+        if self._geometry != (shape.page_size, shape.n_head_kv, shape.head_dim):
             raise ValueError("the cache's pages, heads or head_dim are not the shape's")
         _half(self.k, shape, "the cache")
 
 
+_types = None
+
+
+def _type(t):
+    """(bits, ds_dtype or None for integers) of a device tensor's elements; (0, None) on the host, or of another
+    type than this binding takes."""
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.int32: (32, None), torch.int64: (64, None), torch.uint8: (8, None), torch.int16: (16, None),
+                  torch.float32: (32, DS_F32), torch.bfloat16: (16, DS_BF16), torch.float16: (16, DS_F16)}
+    return _types.get(t.dtype, (0, None)) if t.is_cuda else (0, None)
+
+
 def _half(t, shape, name):
-    import torch
     # 16-bit integers are taken as the bits of the shape's type, as everywhere in this binding
-    if t.dtype != torch.int16 and t.dtype != (torch.float16 if shape.dtype == DS_F16 else torch.bfloat16):
-        raise ValueError(f"{name}: another type than the shape's")
+    bits, kind = _type(t)
+    if bits != 16 or (kind is not None and kind != shape.dtype):
+        raise ValueError(f"{name}: need a device tensor of the shape's type")
 
 
-def _array(t, name, bits, n=None):
+def _array(t, name, bits, n=0):
     """Address of a dense device array of `bits`-bit elements, n of them at least."""
-    if not t.is_cuda or t.element_size() * 8 != bits or not t.is_contiguous() or (n is not None and t.numel() < n):
-        raise ValueError(f"{name}: need a dense device tensor of {bits}-bit elements"
-                         + ("" if n is None else f", {n} or more"))
+    if _type(t)[0] != bits or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: need a dense device tensor of {bits}-bit elements, {n} or more")
     return t.data_ptr()
 
 
-def _table(t):
-    if t.dim() != 2 or not t.is_cuda or t.element_size() != 4 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("block_table: need a device int32 tensor [requests][pages], rows dense")
-    return t.data_ptr(), t.shape[1], t.stride(0)
+def _table(t, rows):
+    if t.dim() != 2 or _type(t)[0] != 32 or (t.size(1) > 1 and t.stride(1) != 1) or t.size(0) < rows:
+        raise ValueError(f"block_table: need a device int32 tensor [{rows} requests][pages], rows dense")
+    return t.data_ptr(), t.size(1), t.stride(0)
 
 
 def page_map(context_lens, new_lens, free_pages, block_table, page_size: int, slots, positions, cu_new, seq_lens,
@@ -477,9 +506,7 @@ def page_map(context_lens, new_lens, free_pages, block_table, page_size: int, sl
     """Pages and places of a step's new tokens (ds_moe_page_map): int32 device tensors, slots int64;
     block_table, slots, positions, cu_new, seq_lens and n_taken are written."""
     R, cap = context_lens.numel(), slots.numel()
-    table, width, stride = _table(block_table)
-    if block_table.shape[0] < R:
-        raise ValueError("block_table has fewer rows than requests")
+    table, width, stride = _table(block_table, R)
     _call(lib().ds_moe_page_map, _array(context_lens, "context_lens", 32), _array(new_lens, "new_lens", 32, R), R,
           page_size, _array(free_pages, "free_pages", 32), free_pages.numel(), table, width, stride,
           _array(slots, "slots", 64), _array(positions, "positions", 32, cap), cap,
@@ -491,12 +518,13 @@ def kv_append(shape: AttentionShape, cache: KVCache, k_new, v_new, slots, stream
     """Copies k_new, v_new [T][n_head_kv][head_dim] (views of any token and head stride) to their slots [T] int64."""
     cache._fits(shape)
     _half(k_new, shape, "k_new")
-    if (k_new.shape[1:] != (shape.n_head_kv, shape.head_dim) or k_new.shape != v_new.shape or k_new.stride() != v_new.stride()
-            or (shape.head_dim > 1 and k_new.stride(2) != 1) or k_new.dtype != v_new.dtype or not (k_new.is_cuda and v_new.is_cuda)):
+    strides = k_new.stride()
+    if (k_new.dim() != 3 or k_new.size(1) != shape.n_head_kv or k_new.size(2) != shape.head_dim or k_new.shape != v_new.shape
+            or strides != v_new.stride() or (shape.head_dim > 1 and strides[2] != 1) or k_new.dtype != v_new.dtype
+            or not v_new.is_cuda):
         raise ValueError("k_new and v_new: device tensors [T][n_head_kv][head_dim] of the same strides, the last axis dense")
-    T = k_new.shape[0]
-    _call(lib().ds_moe_kv_append, shape._c, cache._c, k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0),
-          k_new.stride(1), _array(slots, "slots", 64, T), T, _stream(stream))
+    T = k_new.size(0)
+    _call(lib().ds_moe_kv_append, shape._c, cache._c, k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], _array(slots, "slots", 64, T), T, _stream(stream))
 
 
 def attention_workspace_bytes(shape: AttentionShape, n_requests: int, T: int, max_new: int) -> int:
@@ -506,11 +534,12 @@ def attention_workspace_bytes(shape: AttentionShape, n_requests: int, T: int, ma
 
 
 def _rows(t, shape, name):
-    if (t.shape[1:] != (shape.n_head, shape.head_dim) or not t.is_cuda or (shape.head_dim > 1 and t.stride(2) != 1)
-            or (shape.n_head > 1 and t.stride(1) != shape.head_dim)):
+    s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if (s1 == 0 or t.size(1) != shape.n_head or t.size(2) != shape.head_dim
+            or (shape.head_dim > 1 and s2 != 1) or (shape.n_head > 1 and s1 != shape.head_dim)):
         raise ValueError(f"{name}: need a device tensor [T][n_head][head_dim] with dense heads")
     _half(t, shape, name)
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), s0
 
 
 def paged_attention(shape: AttentionShape, cache: KVCache, block_table, q, cu_new, seq_lens, max_new: int, out, workspace,
@@ -518,16 +547,17 @@ def paged_attention(shape: AttentionShape, cache: KVCache, block_table, q, cu_ne
     """out[T][n_head][head_dim] = attention of the new tokens q over the cache's pages (ds_moe_paged_attention);
     lse: optional fp32 [T][n_head].  block_table, cu_new and seq_lens as page_map writes them."""
     cache._fits(shape)
-    R, T = seq_lens.numel(), q.shape[0]
+    R, T = seq_lens.numel(), q.size(0)
     qp, qs = _rows(q, shape, "q")
     op, os_ = _rows(out, shape, "out")
-    table, width, stride = _table(block_table)
-    if block_table.shape[0] < R or out.shape[0] < T:
-        raise ValueError("block_table or out has too few rows")
-    _call(lib().ds_moe_paged_attention, shape._c, cache._c, table, width, stride, qp, qs, T,
-          _array(cu_new, "cu_new", 32, R + 1), _array(seq_lens, "seq_lens", 32), R, max_new, op, os_,
-          None if lse is None else _array(lse, "lse", 32, T * shape.n_head), _array(workspace, "workspace", 8 * workspace.element_size()),
-          workspace.numel() * workspace.element_size(), _stream(stream))
+    table, width, stride = _table(block_table, R)
+    if out.size(0) < T:
+        raise ValueError("out has too few rows")
+    room = workspace.numel() * workspace.element_size()
+    _call(lib().ds_moe_paged_attention, shape._c, cache._c, table, width, stride, qp, qs, T, _array(cu_new, "cu_new", 32, R + 1),
+          _array(seq_lens, "seq_lens", 32), R, max_new, op, os_,
+          None if lse is None else _array(lse, "lse", 32, T * shape.n_head), _array(workspace, "workspace", _type(workspace)[0]), room,
+          _stream(stream))
 
 
 def attention_path(shape: AttentionShape, cache: KVCache, q, max_new: int) -> int:
@@ -542,18 +572,18 @@ def verify_drafts(target, draft, tokens, cu_new, u_accept, u_sample, out_tokens,
     """Checks drafted tokens against target [T][vocab] (fp32 or bf16 probabilities) from given random numbers
     (ds_moe_verify_drafts).  draft: the drafter's probabilities, rows as target's, or None; out_tokens
     [requests][max_new] and n_accepted [requests] int32 are written."""
-    import torch
-    if target.dim() != 2 or target.dtype not in (torch.float32, torch.bfloat16) or not target.is_cuda or \
-            (target.shape[1] > 1 and target.stride(1) != 1):
+    strides = target.stride()
+    kind = _type(target)[1]
+    if target.dim() != 2 or kind not in (DS_F32, DS_BF16) or (target.size(1) > 1 and strides[1] != 1):
         raise ValueError("target: need a device tensor [T][vocab] of fp32 or bf16, rows dense")
     if draft is not None and (draft.shape != target.shape or draft.dtype != target.dtype or not draft.is_cuda or
-                              (draft.shape[1] > 1 and draft.stride(1) != 1)):
+                              (draft.size(1) > 1 and draft.stride(1) != 1)):
         raise ValueError("draft: need a tensor like target")
-    R, (T, V) = n_accepted.numel(), target.shape
-    if out_tokens.dim() != 2 or out_tokens.shape[0] != R:
+    R, T, V = n_accepted.numel(), target.size(0), target.size(1)
+    if out_tokens.dim() != 2 or out_tokens.size(0) != R:
         raise ValueError("out_tokens: need [requests][max_new]")
-    _call(lib().ds_moe_verify_drafts, target.data_ptr(), target.stride(0), _ptr(draft), 0 if draft is None else draft.stride(0),
-          DS_F32 if target.dtype == torch.float32 else DS_BF16, T, V, _array(tokens, "tokens", 32, T),
-          _array(cu_new, "cu_new", 32, R + 1), R, out_tokens.shape[1], _array(u_accept, "u_accept", 32, T),
+    _call(lib().ds_moe_verify_drafts, target.data_ptr(), strides[0], _ptr(draft), 0 if draft is None else draft.stride(0),
+          kind, T, V, _array(tokens, "tokens", 32, T),
+          _array(cu_new, "cu_new", 32, R + 1), R, out_tokens.size(1), _array(u_accept, "u_accept", 32, T),
           _array(u_sample, "u_sample", 32, R), _array(out_tokens, "out_tokens", 32), _array(n_accepted, "n_accepted", 32),
           _stream(stream))
