@@ -125,34 +125,47 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tpb = 2 * tok;
   asm volatile("griddepcontrol.launch_dependents;");
+  const RawSpan raw0 = first_request<AC_THREADS>(a);  // (under way while the block is set up)
 
-  if (tid == 0) {
-    for (int i = 0; i < KS; ++i) mbar_init(&S.k_full[i], 1), mbar_init(&S.k_empty[i], 1);
-    for (int i = 0; i < VS; ++i) {
-      mbar_init(&S.v_full[i], 1);
-      mbar_init(&S.v_empty[i], 1);
-      mbar_init(&S.v_seen[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.added[i], 4);
-      mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i], 5);
-      mbar_init(&S.o_full[i], 1);
-      pieces.what[2 * blockIdx.x + i] = make_int4(0, 0, 0, 0);
-    }
-    S.segs.init(AC_READERS);
+  if (tid < KS) {
+    mbar_init(&S.k_full[tid], 1);
+    mbar_init(&S.k_empty[tid], 1);
+    fence_mbar_init();
+  } else if (tid >= 32 && tid < 32 + VS) {
+    mbar_init(&S.v_full[tid - 32], 1);
+    mbar_init(&S.v_empty[tid - 32], 1);
+    mbar_init(&S.v_seen[tid - 32], 1);
+    fence_mbar_init();
+  } else if (tid >= 64 && tid < 66) {
+    mbar_init(&S.added[tid - 64], 4);
+    mbar_init(&S.s_full[tid - 64], 1);
+    mbar_init(&S.p_full[tid - 64], 5);
+    mbar_init(&S.o_full[tid - 64], 1);
+    fence_mbar_init();
+  } else if (tid >= 96 && tid < 96 + AT_SEGS) {
+    S.segs.init(tid - 96, AC_READERS);
+    fence_mbar_init();
+  } else if (tid == 128) {
     mbar_init(&S.q_full, 1);
     mbar_init(&S.q_empty, 1);
     mbar_init(&S.drain, 1);
     S.gave_up = 0;
     fence_mbar_init();
+  } else if (tid == 160) {
+    const CUtensorMap *maps[3] = {&tm_q, &tm_k, &tm_v};
+    for (int i = 0; i < 3; ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
   }
+  if (tid == 0) {
+    pieces.what[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    pieces.what[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+  }
+  __syncwarp();
+  if (warp == AC_MMA) tmem_alloc<512>(&S.tmem);
   // query rows that no copy fills stay zero
   for (int i = tid; i < (int)(2 * C::TILE / 16); i += AC_THREADS) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
-  find_start<AC_THREADS>(a, tpb, &S.start, S.part);
+  find_start<AC_THREADS>(a, raw0, tpb, &S.start, S.part);
   __syncwarp();
-  if (warp == AC_MMA) tmem_alloc<512>(&S.tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

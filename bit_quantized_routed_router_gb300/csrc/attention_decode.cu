@@ -68,31 +68,38 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
   Sh &S = *reinterpret_cast<Sh *>(pbuf + 2 * C::P);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;");
+  const RawSpan raw0 = first_request<AD_THREADS>(a);  // (under way while the block is set up)
 
-  if (tid == 0) {
-    for (int i = 0; i < 2 * SLOTS; ++i) {
-      mbar_init(&S.full[i / SLOTS][i % SLOTS], 1);
-      mbar_init(&S.empty[i / SLOTS][i % SLOTS], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
+  if (tid < 2 * SLOTS) {
+    mbar_init(&S.full[tid / SLOTS][tid % SLOTS], 1);
+    mbar_init(&S.empty[tid / SLOTS][tid % SLOTS], 1);
+    fence_mbar_init();
+  } else if (tid >= 32 && tid < 32 + AD_AHEAD) {
+    const int i = tid - 32;
+    mbar_init(&S.s_full[i], 1);
+    if (i < 2) {
       mbar_init(&S.q_full[i], 1);
       mbar_init(&S.q_empty[i], 1);
       mbar_init(&S.p_full[i], 4);
       mbar_init(&S.o_full[i], 1);
-      pieces.what[2 * blockIdx.x + i] = make_int4(0, 0, 0, 0);
     }
-    for (int i = 0; i < AD_AHEAD; ++i) mbar_init(&S.s_full[i], 1);
-    mbar_init(&S.drain, 1);
-    S.gave_up = 0;
+    if (i == 0) mbar_init(&S.drain, 1), S.gave_up = 0;
     fence_mbar_init();
+  } else if (tid == 64) {
+    const CUtensorMap *maps[3] = {&tm_q, &tm_k, &tm_v};
+    for (int i = 0; i < 3; ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
   }
+  if (tid == 0) {
+    pieces.what[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    pieces.what[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+  }
+  __syncwarp();
+  if (warp == AD_MMA) tmem_alloc<C::TMEM>(&S.tmem);
   // query rows that no copy fills stay zero
   for (int i = tid; i < (int)(2 * C::Q / 16); i += AD_THREADS) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
-  find_start<AD_THREADS>(a, TPB, &S.start, S.part);
+  find_start<AD_THREADS>(a, raw0, TPB, &S.start, S.part);
   __syncwarp();
-  __syncthreads();
-  if (warp == AD_MMA) tmem_alloc<C::TMEM>(&S.tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           float top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < N; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
-          if (again || !bar_or(1 + grp, 128, top > AT_SLACK)) break;
+          if (again || (done && !bar_or(1 + grp, 128, top > AT_SLACK))) break;  // (a segment's first tile sets them)
           // raise the maxima to the tile's, and bring the sums down to them
           settle();
           float v[N];

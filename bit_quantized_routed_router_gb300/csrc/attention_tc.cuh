@@ -191,22 +191,46 @@ __device__ __forceinline__ int64_t request_line(const Span &s, int tpb, int wind
   return sum;
 }
 
-// Where a block's stretch of the line begins (request, key head, block of
-// rows, place in the item), and its length.
+// Where a block's stretch of the line begins (request and its span, key head,
+// block of rows, place in the item), and its length.
 struct Start {
   int r, h, b, at;
   int64_t left;
+  Span sp;
 };
+
+// a / b and the rest; most lines are short, and a 64-bit division takes
+// hundreds of cycles.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t &rest) {
+  if (((uint64_t)a | (uint64_t)b) >> 32) {
+    const int64_t q = a / b;
+    rest = a - q * b;
+    return q;
+  }
+  const uint32_t q = (uint32_t)a / (uint32_t)b;
+  rest = (uint32_t)a - q * (uint32_t)b;
+  return q;
+}
+
+// The first request of a thread that find_start() gives `R` requests in turn,
+// loaded ahead of it.
+template <int THREADS>
+__device__ __forceinline__ RawSpan first_request(const AttnArgs &a) {
+  const int per = (a.R + THREADS - 1) / THREADS, r0 = threadIdx.x * per;
+  return r0 < a.R ? request_raw(a.cu, a.seq, r0) : RawSpan{0, 0, 0};
+}
 
 // By all THREADS threads; *out is in shared memory and valid after the
 // caller's next barrier.
 template <int THREADS>
-__device__ __forceinline__ void find_start(const AttnArgs &a, int tpb, Start *out, int64_t *part) {
+__device__ __forceinline__ void find_start(const AttnArgs &a, const RawSpan &raw0, int tpb, Start *out, int64_t *part) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.R + THREADS - 1) / THREADS, r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
   bool bad = false;
-  int64_t mine = 0;
-  for (int r = r0; r < r1; ++r)
+  Span sp0 = request_span(raw0, a.T, a.max_new, a.max_seq, bad);
+  const int64_t line0 = r0 < r1 ? request_line(sp0, tpb, a.window) : 0;
+  int64_t mine = line0;
+  for (int r = r0 + 1; r < r1; ++r)
     mine += request_line(request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad), tpb, a.window);
   int64_t incl = mine;
 #pragma unroll
@@ -227,22 +251,30 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, int tpb, Start *ou
   // no stretch is shorter than an item's overhead and a tile: with little to
   // do the first blocks have a tile each
   const int64_t c = blockIdx.x, blocks = gridDim.x, least = AT_ITEM + 1;
-  const bool full = total >= blocks * least;
-  const int64_t s = full ? total * c / blocks : min(c * least, total);
-  const int64_t e = full ? total * (c + 1) / blocks : min((c + 1) * least, total);
+  int64_t s = min(c * least, total), e = min((c + 1) * least, total);
+  if (total >= blocks * least) {
+    int64_t rest;
+    const int64_t share = divide(total, blocks, rest);  // the first `rest` blocks have one more
+    s = c * share + min(c, rest);
+    e = s + share + (c < rest);
+  }
   if (tid == 0) out->left = e - s;
   if (s >= before && s < before + mine * a.G) {
     int64_t off = s - before;
+    Span sp = sp0;
+    int64_t line = line0;
     for (int r = r0; r < r1; ++r) {
-      const Span sp = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
-      const int64_t line = request_line(sp, tpb, a.window);
+      if (r > r0) {
+        sp = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
+        line = request_line(sp, tpb, a.window);
+      }
       if (off >= line * a.G) {
         off -= line * a.G;
         continue;
       }
       out->r = r;
-      out->h = (int)(off / line);
-      off %= line;
+      out->sp = sp;
+      out->h = (int)divide(off, line, off);
       int b = 0, t0, t1;
       for (;; ++b) {
         tile_range(sp, b * tpb, min(tpb, sp.n - b * tpb), a.window, t0, t1);
@@ -272,8 +304,7 @@ struct Segments {
     index = 0;
     count = 0;
     if (left > 0) {
-      bool bad = false;
-      sp = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
+      sp = s.sp;
       item(a, tpb);
       if (!count) advance(a, tpb);
     }
@@ -329,8 +360,9 @@ constexpr int SEG_START = 1, SEG_END = 2, SEG_LATER = 4;  // has the item's firs
 struct SegRing {
   Seg seg[AT_SEGS];
   uint64_t full[AT_SEGS], empty[AT_SEGS];
-  __device__ __forceinline__ void init(int readers) {
-    for (int i = 0; i < AT_SEGS; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], readers);
+  __device__ __forceinline__ void init(int i, int readers) {
+    mbar_init(&full[i], 1);
+    mbar_init(&empty[i], readers);
   }
   // By one whole warp; the k-th of the stretch.
   __device__ __forceinline__ void put(int k, const Segments &s, bool ok, int *gave_up, unsigned *status) {

@@ -46,18 +46,29 @@ inline int check_kv_cache(const ds_moe_attn_shape *s, const ds_moe_kv_cache *c, 
 struct Span {
   int t0, n, pos0, seq;
 };
+// What it is made of, as it is in memory.
+struct RawSpan {
+  int c0, c1, seq;
+};
+
+__device__ __forceinline__ RawSpan request_raw(const int32_t *__restrict__ cu, const int32_t *__restrict__ seq_lens, int r) {
+  return RawSpan{cu[r], cu[r + 1], seq_lens[r]};
+}
+
+__device__ __forceinline__ Span request_span(const RawSpan &w, int T, int max_new, int64_t max_seq, bool &bad) {
+  Span s;
+  s.t0 = min(max(w.c0, 0), T);
+  const int end = min(max(w.c1, s.t0), T), n = end - s.t0;
+  s.seq = (int)min((int64_t)max(w.seq, 0), max_seq);
+  s.pos0 = s.seq - n;
+  s.n = min(n, max_new);
+  bad = bad || w.c0 != s.t0 || w.c1 != end || w.seq != s.seq || n != s.n;
+  return s;
+}
 
 __device__ __forceinline__ Span request_span(const int32_t *__restrict__ cu, const int32_t *__restrict__ seq_lens, int r,
                                              int T, int max_new, int64_t max_seq, bool &bad) {
-  const int c0 = cu[r], c1 = cu[r + 1], sq = seq_lens[r];
-  Span s;
-  s.t0 = min(max(c0, 0), T);
-  const int end = min(max(c1, s.t0), T), n = end - s.t0;
-  s.seq = (int)min((int64_t)max(sq, 0), max_seq);
-  s.pos0 = s.seq - n;
-  s.n = min(n, max_new);
-  bad = bad || c0 != s.t0 || c1 != end || sq != s.seq || n != s.n;
-  return s;
+  return request_span(request_raw(cu, seq_lens, r), T, max_new, max_seq, bad);
 }
 
 }  // namespace dsm
