@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         else if (a.lse) a.lse[t * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * AT_LN2;
       }
       if (!whole && tid == 0)
-        pieces.what[piece] = make_int4(s.r, s.h, s.b, PIECE_USED | (s.flags & SEG_START ? PIECE_START : 0) | (s.flags & SEG_END ? PIECE_END : 0));
+        pieces.what[piece] = make_int4(s.t0 + s.first, n0, s.h, PIECE_USED | (s.flags & SEG_START ? PIECE_START : 0) | (s.flags & SEG_END ? PIECE_END : 0));
       __syncwarp();
       tc_fence_before();
       S.segs.done(ks);
@@ -602,7 +602,7 @@ cudaError_t launch(const AttnArgs &a, void *ws, cudaStream_t s) {
   const Pieces p = pieces_of(ws, blocks, AC_ROWS, DP);
   attention_chunk_kernel<DP, BF16><<<blocks, AC_THREADS, smem, s>>>(a, p, tq, tk, tv, rows, tok, wide_out);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_join<DP, BF16>(a, p, blocks, AC_ROWS, 2 * tok, tok, s);
+  return launch_join<DP, BF16>(a, p, blocks, AC_ROWS, tok, s);
 }
 
 }  // namespace

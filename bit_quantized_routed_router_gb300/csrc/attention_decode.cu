@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
         }
       }
       if (!whole && tid == 0)
-        pieces.what[piece] = make_int4(s.r, s.h, 0, PIECE_USED | (s.has_start() ? PIECE_START : 0) | (s.has_end() ? PIECE_END : 0));
+        pieces.what[piece] = make_int4(s.sp.t0, s.n, s.h, PIECE_USED | (s.has_start() ? PIECE_START : 0) | (s.has_end() ? PIECE_END : 0));
       warps_bar(3, 256);
     }
   }
@@ -470,7 +470,7 @@ cudaError_t launch(const AttnArgs &a, void *ws, cudaStream_t s) {
   const Pieces p = pieces_of(ws, blocks, N, DP);
   attention_decode_kernel<N, DP, BF16><<<blocks, AD_THREADS, smem, s>>>(a, p, tq, tk, tv, rows);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_join<DP, BF16>(a, p, blocks, N, 1 << 20, 1 << 20, s);
+  return launch_join<DP, BF16>(a, p, blocks, N, 1 << 20, s);
 }
 
 template <int N>

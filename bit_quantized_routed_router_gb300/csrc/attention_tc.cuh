@@ -391,8 +391,9 @@ struct SegRing {
   }
 };
 
-// Pieces: two a block, described by (r, h, b, flags), with `rows` rows of DP
-// sums, and each row's maximum and sum of probabilities.
+// Pieces: two a block, described by (first token, tokens, key head, flags),
+// with `rows` rows of DP sums, and each row's maximum and sum of
+// probabilities.
 constexpr int PIECE_USED = 1, PIECE_START = 2, PIECE_END = 4;
 struct Pieces {
   int4 *what;     // [2 blocks]
@@ -412,84 +413,87 @@ inline Pieces pieces_of(void *ws, int blocks, int rows, int dp) {
   return p;
 }
 
-// One warp a row: the pieces of an item that several blocks share, joined in
-// the order of its keys.  Block x looks at the piece that block x of the
-// attention began and did not end.
+// The pieces of an item that several blocks share, joined in the order of its
+// keys: block x looks at the piece that block x of the attention began and did
+// not end, a warp a row at a time.  Bound by latency, so the descriptions and
+// the statistics that may be needed are all under way at once: lane i has
+// those of the i-th block from x on (the item's further pieces are those
+// blocks' first ones).
+constexpr int JOIN_WARPS = 8;
 template <int DP, bool BF16>
-__global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a, const Pieces p, int rows, int tpb, int tok) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) attention_join_kernel(const AttnArgs a, const Pieces p, int rows, int tok) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = blockIdx.x, blocks = gridDim.x;
   constexpr int PER = DP / 32;
-  int at = 2 * blockIdx.x + 1;
-  int4 w = p.what[at];
-  if ((w.w & (PIECE_USED | PIECE_START | PIECE_END)) != (PIECE_USED | PIECE_START)) {
-    w = p.what[--at];
-    if ((w.w & (PIECE_USED | PIECE_START | PIECE_END)) != (PIECE_USED | PIECE_START)) return;
-  }
-  bool bad = false;
-  const Span sp = request_span(a.cu, a.seq, w.x, a.T, a.max_new, a.max_seq, bad);
-  // rows in tiles of 128, each of `tok` tokens' g heads
-  const int first = w.z * tpb, row = blockIdx.y * 4 + warp, in_tile = row % 128;
-  const int token = row / 128 * tok + in_tile / a.g;
-  if (in_tile >= tok * (int64_t)a.g || token >= min(tpb, sp.n - first)) return;
+  const int4 w0 = p.what[2 * block], w1 = p.what[2 * block + 1];
+  const int own = lane && block + lane < blocks ? p.what[2 * (block + lane)].w : PIECE_END;  // the lane's block's first piece
+  auto begun = [](const int4 &w) { return (w.w & (PIECE_USED | PIECE_START | PIECE_END)) == (PIECE_USED | PIECE_START); };
+  const bool second = begun(w1);
+  if (!second && !begun(w0)) return;
+  const int4 w = second ? w1 : w0;
   // how many pieces: up to the block whose first piece ends the item
-  int n = 1;
-  for (int c = blockIdx.x + 1;; c += 32) {
-    const int e = c + lane < gridDim.x ? p.what[2 * (c + lane)].w : PIECE_END;
-    const unsigned ends = __ballot_sync(0xffffffffu, e & PIECE_END);
+  unsigned ends = __ballot_sync(0xffffffffu, lane && (own & PIECE_END));
+  int n = ends ? __ffs(ends) : 32;
+  for (int c = block + 32; !ends; c += 32) {
+    const int e = c + lane < blocks ? p.what[2 * (c + lane)].w : PIECE_END;
+    ends = __ballot_sync(0xffffffffu, e & PIECE_END);
     n += ends ? __ffs(ends) : 32;
-    if (ends) break;
   }
-  n = min(n, (int)(gridDim.x - blockIdx.x));
-  auto piece = [&](int i) { return (int64_t)(i ? 2 * (blockIdx.x + i) : at) * rows + row; };
-  float m = AT_NONE;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, p.stats[piece(i)].x);
+  n = min(n, blocks - block);
+  for (int row = blockIdx.y * JOIN_WARPS + warp; row < rows; row += gridDim.y * JOIN_WARPS) {
+    // rows in tiles of 128, each of `tok` tokens' g heads
+    const int in_tile = row % 128, token = row / 128 * tok + in_tile / a.g;
+    if (in_tile >= tok * (int64_t)a.g || token >= w.y) continue;
+    auto piece = [&](int i) { return (int64_t)(2 * (block + i) + (i == 0 && second)) * rows + row; };
+    float m = AT_NONE;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.stats[piece(i)].x);
 #pragma unroll
-  for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-  float l = 0.f, o[PER];
+    for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+    float l = 0.f, o[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float2 st = make_float2(AT_NONE, 0.f);
-    if (i0 + lane < n) st = p.stats[piece(i0 + lane)];
-    const float w = ex2(st.x - m), lw = st.y * w;
-    const int k = min(32, n - i0);
+    for (int i = 0; i < PER; ++i) o[i] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float2 st = make_float2(AT_NONE, 0.f);
+      if (i0 + lane < n) st = p.stats[piece(i0 + lane)];
+      const float f = ex2(st.x - m), lf = st.y * f;
+      const int k = min(32, n - i0);
 #pragma unroll 8
-    for (int i = 0; i < k; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      l += __shfl_sync(0xffffffffu, lw, i);
-      const float *src = p.sums + piece(i0 + i) * DP + PER * lane;
+      for (int i = 0; i < k; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        l += __shfl_sync(0xffffffffu, lf, i);
+        const float *src = p.sums + piece(i0 + i) * DP + PER * lane;
 #pragma unroll
-      for (int x = 0; x < PER; x += 2) {
-        const float2 f = *reinterpret_cast<const float2 *>(src + x);
-        o[x] = fmaf(f.x, wi, o[x]);
-        o[x + 1] = fmaf(f.y, wi, o[x + 1]);
+        for (int x = 0; x < PER; x += 2) {
+          const float2 v = *reinterpret_cast<const float2 *>(src + x);
+          o[x] = fmaf(v.x, fi, o[x]);
+          o[x + 1] = fmaf(v.y, fi, o[x + 1]);
+        }
       }
     }
-  }
-  const int64_t t = sp.t0 + first + token;
-  const int h = w.y * a.g + in_tile % a.g;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t *out = a.out + t * a.os + (int64_t)h * a.D + PER * lane;
+    const int64_t t = w.x + token;
+    const int h = w.z * a.g + in_tile % a.g;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t *out = a.out + t * a.os + (int64_t)h * a.D + PER * lane;
 #pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if (PER * lane + i < a.D) out[i] = (uint16_t)pack16<BF16>(o[i] * inv, 0.f);
-  if (a.lse && lane == 0) a.lse[t * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * AT_LN2;
+    for (int i = 0; i < PER; ++i)
+      if (PER * lane + i < a.D) out[i] = (uint16_t)pack16<BF16>(o[i] * inv, 0.f);
+    if (a.lse && lane == 0) a.lse[t * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * AT_LN2;
+  }
 }
 
 // Behind an attention kernel of `blocks` blocks; its set-up overlaps that kernel's end.
 template <int DP, bool BF16>
-cudaError_t launch_join(const AttnArgs &a, const Pieces &p, int blocks, int rows, int tpb, int tok, cudaStream_t s) {
+cudaError_t launch_join(const AttnArgs &a, const Pieces &p, int blocks, int rows, int tok, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks, rows / 4);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(blocks, std::min(rows / JOIN_WARPS, 8));
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, BF16>, a, p, rows, tpb, tok);
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, BF16>, a, p, rows, tok);
 }
 
 // The keys or values as a 4-D map {element, row of a page, head, page} with
