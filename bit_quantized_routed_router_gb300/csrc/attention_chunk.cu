@@ -111,9 +111,49 @@ struct Ahead {
   }
 };
 
+template <int DP>
+__device__ __noinline__ void scale_sums(uint32_t t_o, float by) {
+#pragma unroll 1
+  for (int c = 0; c < DP; c += 16) {
+    float o[16];
+    tmem_ld16(t_o + c, o);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] *= by;
+    tmem_st16(t_o + c, o);
+  }
+}
+
+// Adds to a row's sums the values of a tile that are not finite and that the
+// row sees: columns [lo, hi).  (Rare: kept out of the loop's code.)
+template <int DP, bool BF16>
+__device__ __noinline__ void add_odd(const uint8_t *vt, const uint32_t *odd, int lo, int hi, uint32_t t_o) {
+  for (int k = 0; k < AT_KEYS; ++k) {
+    if (!(odd[k >> 5] >> (k & 31) & 1u)) continue;
+    const bool sees = k >= lo && k < hi;
+#pragma unroll 1
+    for (int c = 0; c < DP; c += 16) {
+      float o[16];
+      tmem_ld16(t_o + c, o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int d = c + e;
+        const uint16_t v = *reinterpret_cast<const uint16_t *>(vt + d / 64 * (AT_KEYS * 128) + k * 128 +
+                                                               ((((d & 63) >> 3) ^ (k & 7)) << 4) + (d & 7) * 2);
+        if (sees && not_finite2<BF16>(v)) o[e] += BF16 ? bf16_to_f32(v) : fp16_to_f32(v);
+      }
+      tmem_st16(t_o + c, o);
+    }
+  }
+}
+
+// (once a block: kept out of the code that the loops share a cache with)
+__device__ __noinline__ void chunk_start(const AttnArgs &a, const RawSpan raw0, int tpb, Start *out, int64_t *part) {
+  find_start<AC_THREADS>(a, raw0, tpb, out, part);
+}
+
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(AC_THREADS, 1)
-    attention_chunk_kernel(const AttnArgs a, const Pieces pieces, const __grid_constant__ CUtensorMap tm_q,
+    attention_chunk_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Pieces pieces, const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, int rows,
                            int tok, bool wide_out) {
   using C = AcCfg<DP>;
@@ -164,7 +204,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
   // query rows that no copy fills stay zero
   for (int i = tid; i < (int)(2 * C::TILE / 16); i += AC_THREADS) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
-  find_start<AC_THREADS>(a, raw0, tpb, &S.start, S.part);
+  chunk_start(a, raw0, tpb, &S.start, S.part);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -435,16 +475,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
           const float to = fmaxf(m, top), keep = ex2(m - to);
           l *= keep;
           m = to;
-          if (done) {
-#pragma unroll 1
-            for (int c = 0; c < DP; c += 16) {
-              float o[16];
-              tmem_ld16(t_o + c, o);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= keep;
-              tmem_st16(t_o + c, o);
-            }
-          }
+          if (done) scale_sums<DP>(t_o, keep);
         }
         const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
@@ -471,23 +502,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
           const int sl = f % VS;
           at_wait_warp(&S.v_seen[sl], f / VS & 1, &S.gave_up, a.status);
           if (S.odd[sl][0] | S.odd[sl][1] | S.odd[sl][2] | S.odd[sl][3]) {
-            const uint8_t *vt = vring + sl * C::TILE;
-            for (int k = 0; k < AT_KEYS; ++k) {
-              if (!(S.odd[sl][k >> 5] >> (k & 31) & 1u)) continue;
-              const bool sees = k >= lo && k < hi;
-              for (int c = 0; c < DP; c += 16) {
-                float o[16];
-                tmem_ld16(t_o + c, o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const int d = c + e;
-                  const uint16_t v = *reinterpret_cast<const uint16_t *>(vt + d / 64 * (AT_KEYS * 128) + k * 128 +
-                                                                         ((((d & 63) >> 3) ^ (k & 7)) << 4) + (d & 7) * 2);
-                  if (sees && not_finite2<BF16>(v)) o[e] += BF16 ? bf16_to_f32(v) : fp16_to_f32(v);
-                }
-                tmem_st16(t_o + c, o);
-              }
-            }
+            add_odd<DP, BF16>(vring + sl * C::TILE, S.odd[sl], lo, hi, t_o);
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.added[grp]);
           }

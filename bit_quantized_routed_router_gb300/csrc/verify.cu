@@ -49,31 +49,26 @@ __device__ __forceinline__ float clean(float p, bool &bad) {
   return p > 1.f ? 1.f : 0.f;
 }
 
-// Weights of 8 entries x0, x0 + step, ... of a row that is sampled from:
-// max(p - q, 0) with the target's p and the draft's q when q is given, or the
-// target's alone, but none at the draft `sure`.  All loads are under way
-// before the first is used; ALL: every entry is in the vocabulary.
+// Probabilities of 8 entries x0, x0 + step, ... of a row, all loads under way
+// at once; ALL: every entry is in the vocabulary.
+template <bool BF16, bool ALL>
+__device__ __forceinline__ void load8(const void *base, int64_t row, int x0, int step, int V, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = base && (ALL || x0 + i * step < V) ? prob<BF16>(base, row + x0 + i * step) : 0.f;
+}
+
+// Weights of those entries of a row that is sampled from: max(p - q, 0) with
+// the target's p and the draft's q (zeros where it is not to count), or none
+// at the draft `sure`.
 //
 // A weight is a whole number of 2^-44 units, hi * 2^22 + lo.  With q held to
 // at most p the difference is s plus an exact error e (Dekker's fast two-sum);
 // adding 1.5 * 2^23 rounds to whole numbers, which are the low bits of the
 // sum.  Sums of such numbers are exact, so no order of adding changes the
 // token that is drawn; fp64 adds would be slower than HBM here.
-template <bool BF16, bool ALL>
-__device__ __forceinline__ int64_t weights(const void *p, int64_t prow, const void *q, int64_t qrow, int sure, int x0, int step,
-                                           int V, int64_t each[8], bool &bad) {
+__device__ __forceinline__ int64_t weights(float pv[8], float qv[8], int sure, int x0, int step, int64_t each[8], bool &bad) {
   constexpr float MAGIC = 12582912.f, UNIT = 4194304.f;  // 1.5 * 2^23, 2^22
   constexpr uint32_t MAGIC_BITS = 0x4B400000u;
-  float pv[8], qv[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) pv[i] = ALL || x0 + i * step < V ? prob<BF16>(p, prow + x0 + i * step) : 0.f;
-  if (q) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) qv[i] = ALL || x0 + i * step < V ? prob<BF16>(q, qrow + x0 + i * step) : 0.f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) qv[i] = 0.f;
-  }
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, max(__float_as_uint(pv[i]), __float_as_uint(qv[i])));
@@ -176,11 +171,23 @@ __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const V
     int64_t total = 0, before = 0, own = 0;
     for (int turn = 0; turn < 2; ++turn) {
       int64_t sum = 0;
-      for (int c = warp; c < mine; c += VD_WARPS) {
+      float pv[8], qv[8], pn[8], qn[8];
+      auto load = [&](int c, float p8[8], float q8[8]) {
         const int x0 = (first + c) * VD_CHUNK + lane;
-        const int64_t s = warp_sum64((first + c + 1) * VD_CHUNK <= a.V
-                                         ? weights<BF16, true>(a.p, prow, q, qrow, sure, x0, 32, a.V, nullptr, bad)
-                                         : weights<BF16, false>(a.p, prow, q, qrow, sure, x0, 32, a.V, nullptr, bad));
+        if ((first + c + 1) * VD_CHUNK <= a.V) {
+          load8<BF16, true>(a.p, prow, x0, 32, a.V, p8);
+          load8<BF16, true>(q, qrow, x0, 32, a.V, q8);
+        } else {
+          load8<BF16, false>(a.p, prow, x0, 32, a.V, p8);
+          load8<BF16, false>(q, qrow, x0, 32, a.V, q8);
+        }
+      };
+      if (warp < mine) load(warp, pn, qn);
+      for (int c = warp; c < mine; c += VD_WARPS) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pv[i] = pn[i], qv[i] = qn[i];
+        if (c + VD_WARPS < mine) load(c + VD_WARPS, pn, qn);  // (the next chunk's loads, before this one's arithmetic)
+        const int64_t s = warp_sum64(weights(pv, qv, sure, (first + c) * VD_CHUNK + lane, 32, nullptr, bad));
         if (lane == 0) chunk[c] = s;
         sum += s;
       }
@@ -231,7 +238,10 @@ __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const V
         const int x0 = (first + at) * VD_CHUNK + lane * 8;
         bool none = false;
         int64_t each[8];
-        const int64_t v = weights<BF16, false>(a.p, prow, q, qrow, sure, x0, 1, a.V, each, none), incl = warp_scan64(v);
+        float pv[8], qv[8];
+        load8<BF16, false>(a.p, prow, x0, 1, a.V, pv);
+        load8<BF16, false>(q, qrow, x0, 1, a.V, qv);
+        const int64_t v = weights(pv, qv, sure, x0, 1, each, none), incl = warp_scan64(v);
         const unsigned pass = __ballot_sync(0xffffffffu, before + incl > thr);
         if (pass && lane == __ffs(pass) - 1) {
           int64_t run = before + incl - v;
