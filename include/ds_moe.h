@@ -420,14 +420,16 @@ typedef struct {
   int32_t dtype;     /* DS_BF16 or DS_F16: q, the cache, the new keys and
                         values, and out                                      */
   float scale;       /* multiplies q k^T; 0: 1/sqrt(head_dim)                */
-  int32_t window;    /* keys that a token sees, itself included; 0: all      */
+  int32_t window;    /* keys that a token sees, itself included; 0: all
+                        (sequences are shorter than 2^30)                    */
 } ds_moe_attn_shape;
 
 /* Pages of keys and values: element (page, row, head, d) of either is at
  * page * page_stride + row * row_stride + head * head_stride + d, in
  * elements, the last axis dense.  Any order of the axes is fine (pages of
- * rows or of heads; both in one buffer).  The fast kernels want the bases
- * 16-byte aligned and the strides multiples of 8. */
+ * rows or of heads; both in one buffer).  The tensor-core attention wants the
+ * bases (and q) 16-byte aligned, the strides, head_dim and page_size multiples
+ * of 8, and at most 128 query heads a key head; others run on CUDA cores. */
 typedef struct {
   void *k, *v;
   int64_t n_pages;
@@ -508,9 +510,9 @@ int ds_moe_verify_drafts(const void *target, int64_t target_stride, const void *
  * launched): one of the DS_ATTN_* values, or a negative ds_status. */
 enum {
   DS_ATTN_GENERIC = 0, /* any strides, page and head sizes: CUDA cores        */
-  DS_ATTN_DECODE = 1,  /* few query rows a key head: keys as the rows of the
-                          tensor-core tiles                                  */
-  DS_ATTN_CHUNK = 2    /* many query rows: queries as the rows               */
+  DS_ATTN_DECODE = 1,  /* up to 32 query rows (max_new * n_head / n_head_kv)
+                          a key head: keys as the rows of tensor-core tiles  */
+  DS_ATTN_CHUNK = 2    /* more query rows: queries as the rows               */
 };
 int ds_moe_attention_path(const ds_moe_attn_shape *shape, const ds_moe_kv_cache *cache, const void *q,
                           int64_t q_stride, int32_t max_new);

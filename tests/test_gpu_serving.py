@@ -296,6 +296,28 @@ def test_attention_long_sequences(page, D, new, window):
     assert bool(((lse.double() - z.reshape(new, H)).abs() <= score + sums + 2.0 ** -20).all())
 
 
+def test_attention_path():
+    """Which kernel serves which geometry: the fast ones want 8-element alignment, pages of whole 8-row groups and heads
+    of a multiple of 8; up to 32 query rows a key head the decode kernel, above it the chunk kernel."""
+    def path(new, H=8, G=2, D=128, page=16, **kw):
+        c = ref.Case([20], [new], H, G, D, page, **kw).put()
+        return ds.attention_path(shape_of(c), ds.KVCache(c.k, c.v), c.q, new)
+    assert path(1) == path(8) == path(1, H=32, G=1) == path(2, D=64, page=8, layout="heads") == ds.ATTN_DECODE
+    assert path(9) == path(1, H=33, G=1) == path(1, H=128, G=1) == path(300, D=72, layout="both") == ds.ATTN_CHUNK
+    assert path(1, page=20) == path(1, D=36) == path(9, layout="odd", D=64) == path(1, H=129, G=1) == ds.ATTN_GENERIC
+
+
+def test_example_runs():
+    import importlib.util
+    import os
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serving_step.py")
+    spec = importlib.util.spec_from_file_location("serving_step", at)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    kept = example.run(steps=5)
+    assert all(len(k) > 40 for k in kept)
+
+
 # -------------------------------------------------------------------- page map
 
 
