@@ -415,13 +415,17 @@ inline Pieces pieces_of(void *ws, int blocks, int rows, int dp) {
 
 // The pieces of an item that several blocks share, joined in the order of its
 // keys: block x looks at the piece that block x of the attention began and did
-// not end, a warp a row at a time.  Bound by latency, so the descriptions and
-// the statistics that may be needed are all under way at once: lane i has
-// those of the i-th block from x on (the item's further pieces are those
-// blocks' first ones).
-constexpr int JOIN_WARPS = 8;
+// not end (the item's further pieces are the following blocks' first ones).
+// Bound by latency: where there are few pieces a warp joins a row; where there
+// are many (one request's long sequence under one key head is shared by all
+// blocks) the eight warps of a block share a row's pieces, and then their
+// results (152 pieces of 100,000 keys: 77 us with a warp a row, 15 us so,
+// from a cold cache).
+constexpr int JOIN_WARPS = 8, JOIN_FEW = 8, JOIN_BLOCKS = 32;
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) attention_join_kernel(const AttnArgs a, const Pieces p, int rows, int tok) {
+  __shared__ float2 part_stats[JOIN_WARPS];
+  __shared__ float part_sums[JOIN_WARPS][DP];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = blockIdx.x, blocks = gridDim.x;
   constexpr int PER = DP / 32;
@@ -440,28 +444,36 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attention_join_kernel(const A
     n += ends ? __ffs(ends) : 32;
   }
   n = min(n, blocks - block);
-  for (int row = blockIdx.y * JOIN_WARPS + warp; row < rows; row += gridDim.y * JOIN_WARPS) {
+  const bool shared = n > JOIN_FEW;
+  const int first = shared ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp, step = gridDim.y * (shared ? 1 : JOIN_WARPS);
+  // pieces begin, begin + stride, ...
+  const int begin = shared ? warp : 0, stride = shared ? JOIN_WARPS : 1;
+  for (int row = first; row < rows; row += step) {
     // rows in tiles of 128, each of `tok` tokens' g heads
     const int in_tile = row % 128, token = row / 128 * tok + in_tile / a.g;
     if (in_tile >= tok * (int64_t)a.g || token >= w.y) continue;
     auto piece = [&](int i) { return (int64_t)(2 * (block + i) + (i == 0 && second)) * rows + row; };
-    float m = AT_NONE;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.stats[piece(i)].x);
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    float l = 0.f, o[PER];
+    const int mine = (n - begin + stride - 1) / stride;
+    float m = AT_NONE, l = 0.f, o[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) o[i] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
+    for (int i0 = 0; i0 < mine; i0 += 32) {
       float2 st = make_float2(AT_NONE, 0.f);
-      if (i0 + lane < n) st = p.stats[piece(i0 + lane)];
-      const float f = ex2(st.x - m), lf = st.y * f;
-      const int k = min(32, n - i0);
+      if (i0 + lane < mine) st = p.stats[piece(begin + (i0 + lane) * stride)];
+      float to = fmaxf(m, st.x);
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, i));
+      const float keep = ex2(m - to), f = ex2(st.x - to), lf = st.y * f;
+      m = to;
+      l *= keep;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] *= keep;
+      const int k = min(32, mine - i0);
 #pragma unroll 8
       for (int i = 0; i < k; ++i) {
         const float fi = __shfl_sync(0xffffffffu, f, i);
         l += __shfl_sync(0xffffffffu, lf, i);
-        const float *src = p.sums + piece(i0 + i) * DP + PER * lane;
+        const float *src = p.sums + piece(begin + (i0 + i) * stride) * DP + PER * lane;
 #pragma unroll
         for (int x = 0; x < PER; x += 2) {
           const float2 v = *reinterpret_cast<const float2 *>(src + x);
@@ -469,6 +481,24 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attention_join_kernel(const A
           o[x + 1] = fmaf(v.y, fi, o[x + 1]);
         }
       }
+    }
+    if (shared) {
+      if (lane == 0) part_stats[warp] = make_float2(m, l);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) part_sums[warp][PER * lane + i] = o[i];
+      __syncthreads();
+      if (warp == 0) {
+        for (int v = 1; v < JOIN_WARPS; ++v) {
+          const float2 st = part_stats[v];
+          const float to = fmaxf(m, st.x), keep = ex2(m - to), f = ex2(st.x - to);
+          l = l * keep + st.y * f;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) o[i] = o[i] * keep + part_sums[v][PER * lane + i] * f;
+          m = to;
+        }
+      }
+      __syncthreads();
+      if (warp) continue;
     }
     const int64_t t = w.x + token;
     const int h = w.z * a.g + in_tile % a.g;
@@ -485,7 +515,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attention_join_kernel(const A
 template <int DP, bool BF16>
 cudaError_t launch_join(const AttnArgs &a, const Pieces &p, int blocks, int rows, int tok, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks, std::min(rows / JOIN_WARPS, 8));
+  cfg.gridDim = dim3(blocks, std::min(rows, JOIN_BLOCKS));
   cfg.blockDim = dim3(JOIN_WARPS * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
