@@ -17,7 +17,10 @@
 //                   one a query tile; where there is one (the request's
 //                   tokens fit it), a key tile is one turn, and the groups'
 //                   sums are joined at the segment's end;
-//   MMA thread      per turn: O += P V, then S of the turn after the next;
+//   MMA thread      per turn: O += P V, then the S that takes P's place (that
+//                   of two turns on; for head_dim <= 64, whose sums leave room
+//                   for a third tile of scores, of three turns on: a group's
+//                   next scores are then there when it has done the last);
 //   two producer warps         keys (and the query rows), values;
 //   gate warp       in tiles that not every row sees it clears the values that
 //                   none sees and looks for infinities and NaN in the others;
@@ -28,7 +31,17 @@
 //                   anything else, and a warp that runs alone takes hundreds
 //                   of cycles for a little bookkeeping.
 //
-// Maxima are raised lazily (AT_SLACK), by warp.
+// Maxima are raised lazily (AT_SLACK), by warp.  Probabilities are rounded to
+// the 16-bit type of the values, which the second product takes; their sums,
+// the maxima and the accumulators are 32 bits.
+//
+// Measured: 2048 tokens x 32 heads (8 key heads) of 128 over 30,011 keys 690 us,
+// 1.50 PFLOP/s, at the power limit of the board; over 8000 keys 228 us, 58 % of
+// the tensor cores' cycles.  head_dim 64 over 8000 keys 185 us (201 with two
+// tiles of scores): a turn is 1300 cycles there, of which 512 are products and
+// 512 exponentials; what is left is the way of a turn through the warps.  17
+// requests of 3 to 666 tokens, a window of 1024, 76 us; 29 requests of 1 to 6
+// tokens, 7 query heads a key head, over 34 to 4993 keys 32 us.
 #include "attention_tc.cuh"
 
 namespace dsm {
@@ -38,12 +51,26 @@ constexpr int AC_THREADS = 384;
 constexpr int AC_MMA = 8, AC_KEYS = 9, AC_VALUES = 10, AC_GATE = 11;
 constexpr int AC_READERS = 10;  // warps that read all segments: softmax, values, gate
 constexpr int AC_ROWS = 256;
+// Turns that an item costs besides its own: its sums' way out, and the wait
+// for its first scores (17 requests of 3 to 666 tokens: 78 us with 3, 76 with
+// 4, 75 with 6; 29 requests of 1 to 6: 31, 32, 33).
+constexpr int AC_ITEM = 4;
 constexpr int AC_HEAD = 3 * 1024;  // bytes of a block's barriers and small arrays
 
 template <int DP>
 struct AcCfg {
   static constexpr uint32_t TILE = AT_KEYS * DP * 2;  // keys, values, or a query tile
   static constexpr int KS = DP == 128 ? 2 : 4, VS = DP == 128 ? 3 : 4;
+  static constexpr int QS = DP == 128 ? 1 : 2;  // segments' query rows
+  static constexpr int NB = DP == 128 ? 2 : 3;  // tiles of scores: what the sums leave of tensor memory
+  // Scores that a thread takes at a time.  The wider loop is the faster one in
+  // steady state, and its masks are then better out of its way; but a smaller
+  // one costs less where the code changes often, at tiles with masks and the
+  // ends of segments, which is most of the work of a batch of short chunks
+  // (2048 tokens over 30,011 keys, head_dim 128: 677 us with 64, 718 with 32;
+  // 17 requests of 3 to 666 tokens, head_dim 64: 94 us with 64, 79 with 32, and 105 and 99 with head_dim 128).
+  static constexpr int WIDE = DP == 128 ? 64 : 32;
+  static constexpr int SUMS = NB * 128;         // column of the first group's sums
 };
 
 // What a turn is, for the MMA thread: its value slot, and of the scores that
@@ -61,27 +88,28 @@ enum : uint32_t {
   TURN_FREE_V = 1u << 8,
   TURN_SUMS = 1u << 9,     // the group's last of the segment
   TURN_LAST = 1u << 10,    // the stretch's last
+  TURN_Q_SLOT = 1u << 11,
   TURN_K_SLOT = 1u << 12,  // times the slot
   TURN_V_SLOT = 1u << 16
 };
 
-template <int KS, int VS>
+template <int KS, int VS, int QS>
 struct AcShared {
   uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
   uint64_t v_seen[VS];               // looked at
   uint64_t added[2];                 // by group: values that are not finite are in its sums
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[QS], q_empty[QS], s_full[4], p_full[4], o_full[4], drain;  // (of turn j at j mod 4)
   uint32_t odd[VS][4];  // keys whose values are not all finite
   float2 stats[2][128]; // maximum and sum of a row, by group
   SegRing segs;
-  uint32_t turns[4];    // turn j's word at j mod 4
+  uint32_t turns[8];    // turn j's word at j mod 8
   int64_t part[AC_THREADS / 32];
   Start start;
   uint32_t tmem;
   int gave_up;
 };
 
-// The walk over turns that the scores take, two turns ahead of the sums.
+// The walk over turns that the scores take, NB turns ahead of the sums.
 struct Ahead {
   int k, count, i, f;  // segment, its tiles, tile of it, tile of the stretch
   bool two, half;      // two turns a tile; the first of them is done
@@ -93,12 +121,12 @@ struct Ahead {
     i = 0;
   }
   // The scores of the turn: their part of a word.
-  template <int KS>
+  template <int KS, int QS>
   __device__ __forceinline__ uint32_t word(int w) const {
     if (!count) return 0;
     const bool last = two ? half : true;  // of the tile
     return TURN_SCORES | (half ? 0u : TURN_WAIT_K | (f / KS & 1 ? TURN_K_PAR : 0u)) |
-           (!half && i == 0 ? TURN_WAIT_Q | (k & 1 ? TURN_Q_PAR : 0u) : 0u) | (two && w ? TURN_Q_TILE : 0u) |
+           (!half && i == 0 ? TURN_WAIT_Q | (k / QS & 1 ? TURN_Q_PAR : 0u) : 0u) | (k % QS ? TURN_Q_SLOT : 0u) | (two && w ? TURN_Q_TILE : 0u) |
            (last ? TURN_FREE_K : 0u) | (last && i + 1 == count ? TURN_FREE_Q : 0u) | (uint32_t)(f % KS) * TURN_K_SLOT;
   }
   // To the next turn.
@@ -110,6 +138,24 @@ struct Ahead {
     if (++i == count) segment(ring, k + 1, tok, status);
   }
 };
+
+__device__ __forceinline__ void load_scores(uint32_t t, float (&v)[32]) { tmem_ld32(t, v); }
+__device__ __forceinline__ void load_scores(uint32_t t, float (&v)[64]) { tmem_ld64(t, v); }
+
+// Replaces a row's scores outside of columns [lo, hi) by -infinity.
+__device__ __noinline__ void mask_scores(uint32_t t_s, int lo, int hi) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < AT_KEYS; c0 += 32) {
+    const uint32_t see = bits(lo - c0, hi - c0);
+    if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+    float x[32];
+    tmem_ld32(t_s + c0, x);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) x[c] = see >> c & 1u ? x[c] : -INFINITY;
+    tmem_st32(t_s + c0, x);
+  }
+  tmem_st_wait();
+}
 
 template <int DP>
 __device__ __noinline__ void scale_sums(uint32_t t_o, float by) {
@@ -147,8 +193,8 @@ __device__ __noinline__ void add_odd(const uint8_t *vt, const uint32_t *odd, int
 }
 
 // (once a block: kept out of the code that the loops share a cache with)
-__device__ __noinline__ void chunk_start(const AttnArgs &a, const RawSpan raw0, int tpb, Start *out, int64_t *part) {
-  find_start<AC_THREADS>(a, raw0, tpb, out, part);
+__device__ __noinline__ void chunk_start(const AttnArgs &a, const RawSpan raw0, const Plan plan, Start *out, int64_t *part) {
+  find_start<AC_THREADS>(a, raw0, plan, out, part);
 }
 
 template <int DP, bool BF16>
@@ -157,13 +203,13 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                            const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, int rows,
                            int tok, bool wide_out) {
   using C = AcCfg<DP>;
-  constexpr int KS = C::KS, VS = C::VS;
+  constexpr int KS = C::KS, VS = C::VS, QS = C::QS;
   extern __shared__ __align__(1024) uint8_t smem_tiles[];  // (the period of the 128-byte swizzle)
-  typedef AcShared<KS, VS> Sh;
+  typedef AcShared<KS, VS, QS> Sh;
   Sh &S = *reinterpret_cast<Sh *>(smem_tiles);
-  uint8_t *qbuf = smem_tiles + AC_HEAD, *kring = qbuf + 2 * C::TILE, *vring = kring + KS * C::TILE;
+  uint8_t *qbuf = smem_tiles + AC_HEAD, *kring = qbuf + 2 * QS * C::TILE, *vring = kring + KS * C::TILE;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tpb = 2 * tok;
+  const Plan plan = {2 * tok, tok, AC_ITEM};
   asm volatile("griddepcontrol.launch_dependents;");
   const RawSpan raw0 = first_request<AC_THREADS>(a);  // (under way while the block is set up)
 
@@ -178,16 +224,20 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     fence_mbar_init();
   } else if (tid >= 64 && tid < 66) {
     mbar_init(&S.added[tid - 64], 4);
-    mbar_init(&S.s_full[tid - 64], 1);
-    mbar_init(&S.p_full[tid - 64], 5);
-    mbar_init(&S.o_full[tid - 64], 1);
+    for (int i = tid - 64; i < 4; i += 2) {
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 5);
+      mbar_init(&S.o_full[i], 1);
+    }
     fence_mbar_init();
   } else if (tid >= 96 && tid < 96 + AT_SEGS) {
     S.segs.init(tid - 96, AC_READERS);
     fence_mbar_init();
   } else if (tid == 128) {
-    mbar_init(&S.q_full, 1);
-    mbar_init(&S.q_empty, 1);
+    for (int i = 0; i < QS; ++i) {
+      mbar_init(&S.q_full[i], 1);
+      mbar_init(&S.q_empty[i], 1);
+    }
     mbar_init(&S.drain, 1);
     S.gave_up = 0;
     fence_mbar_init();
@@ -202,44 +252,46 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
   __syncwarp();
   if (warp == AC_MMA) tmem_alloc<512>(&S.tmem);
   // query rows that no copy fills stay zero
-  for (int i = tid; i < (int)(2 * C::TILE / 16); i += AC_THREADS) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < (int)(2 * QS * C::TILE / 16); i += AC_THREADS) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
-  chunk_start(a, raw0, tpb, &S.start, S.part);
+  chunk_start(a, raw0, plan, &S.start, S.part);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = S.tmem;  // scores of the query tiles at 0 and 128, sums at 256 and 384
+  const uint32_t tmem = S.tmem;  // scores of turn j at (j mod NB) 128, sums of group i at SUMS + i DP
   // whether some of n rows' tokens, the first at position p, does not see some key of a tile
   auto edge_of = [&](int p, int n, int j0) { return j0 + AT_KEYS - 1 > p || (a.window && j0 < p + n - a.window); };
 
   if (warp == AC_KEYS) {
     // -------------------------------- segments, query rows and keys ------
     Segments s;
-    s.init(a, tpb, S.start);
+    s.init(a, plan, S.start);
     bool ok = true, bad = false;
-    int segs = 0, f = 0, i = 0;
+    int segs = 0, asked = 0, f = 0, i = 0;  // segments, those whose query rows are under way, tiles
     TileRuns now, later;
     if (s.count) now.find(a, s, s.tile, rows);
     for (; s.count; ++f) {
       const int head = s.h;
       if (i == 0) {
         S.segs.put(segs, s, ok, &S.gave_up, a.status);
-        if (lane == 0 && segs && !at_wait(&S.q_empty, (segs & 1) ^ 1, &S.gave_up, a.status)) ok = false;
+        const int q = segs % QS;
+        if (lane == 0 && segs >= QS && !at_wait(&S.q_empty[q], (segs / QS & 1) ^ 1, &S.gave_up, a.status)) ok = false;
         ++segs;
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        ++asked;
         if (lane == 0) {
           const int tiles = s.n > tok ? 2 : 1;
-          mbar_arrive_expect_tx(&S.q_full, tiles * tok * a.g * DP * 2);
+          mbar_arrive_expect_tx(&S.q_full[q], tiles * tok * a.g * DP * 2);
           for (int w = 0; w < tiles; ++w)
 #pragma unroll
             for (int x = 0; x < DP; x += 64)
-              tma_load_3d(qbuf + w * C::TILE + x / 64 * (128 * 128), &tm_q, x, s.h * a.g, s.sp.t0 + s.first + w * tok, &S.q_full);
+              tma_load_3d(qbuf + (2 * q + w) * C::TILE + x / 64 * (128 * 128), &tm_q, x, s.h * a.g, s.sp.t0 + s.first + w * tok, &S.q_full[q]);
         }
         __syncwarp();
       }
       if (++i == s.count) {
-        s.next(a, tpb);
+        s.next(a);
         i = 0;
       }
       if (s.count) later.find(a, s, s.tile + i, rows);
@@ -254,7 +306,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     if (lane == 0) {  // every copy of this warp has landed before the block ends
       int off = 0;
       for (int g = max(0, f - KS); g < f; ++g) at_wait(&S.k_full[g % KS], g / KS & 1, &off, a.status);
-      if (segs && ok) at_wait(&S.q_full, (segs - 1) & 1, &off, a.status);
+      for (int g = max(0, asked - QS); g < asked; ++g) at_wait(&S.q_full[g % QS], g / QS & 1, &off, a.status);
     }
   } else if (warp == AC_VALUES) {
     // ------------------------------------------------------------ values --
@@ -289,7 +341,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     int f = 0, turn = 0, adds[2] = {0, 0};
     Ahead z{};
     z.segment(S.segs, 0, tok, a.status);
-    for (int j = 0; j < 2; ++j) z.step(S.segs, tok, a.status);
+    for (int j = 0; j < C::NB; ++j) z.step(S.segs, tok, a.status);
     for (int k = 0;; ++k) {
       const Seg s = S.segs.get(k, a.status);
       if (!s.count) break;
@@ -310,9 +362,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             if (j >= see_hi || j < see_lo) {
 #pragma unroll
               for (int x = 0; x < DP / 8; ++x)
-                *reinterpret_cast<uint4 *>(vr + x / 8 * (AT_KEYS * 128) + x % 8 * 16) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(vr + row_word(x, lane)) = make_uint4(0, 0, 0, 0);
             } else if (j >= all_hi || j < all_lo) {
-              odd = not_finite_row<BF16, DP / 8>(vr);
+              odd = not_finite_row<BF16, DP / 8>(vr, lane);
             }
             m[k] = __ballot_sync(0xffffffffu, odd);
             any |= m[k];
@@ -341,17 +393,17 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
           mbar_arrive(&S.v_seen[sl]);  // (its phases go with the tiles)
         }
         for (int t = 0; t < (two ? 2 : 1); ++t) {
-          const int j = turn + t, w = j & 1;
+          const int j = turn + t;
           const bool tile_end = !two || t, sums = i + (two ? 1 : 2) >= s.count;
-          uint32_t word = z.word<KS>(w) | (uint32_t)sl * TURN_V_SLOT | (tile_end ? TURN_FREE_V : 0u) | (sums ? TURN_SUMS : 0u);
+          uint32_t word = z.word<KS, QS>((j + C::NB) & 1) | (uint32_t)sl * TURN_V_SLOT | (tile_end ? TURN_FREE_V : 0u) | (sums ? TURN_SUMS : 0u);
           z.step(S.segs, tok, a.status);
           // (the stretch's last turn has no other behind it: none after the
           // next, and the segment after this one is its end)
           if (tile_end && i + 1 == s.count && !S.segs.get(k + 1, a.status).count) word |= TURN_LAST;
-          if (j >= 2) at_wait(&S.p_full[w], ((j >> 1) - 1) & 1, &S.gave_up, a.status);  // the arrival is for this turn
+          if (j >= 4) at_wait(&S.p_full[j & 3], ((j >> 2) - 1) & 1, &S.gave_up, a.status);  // the arrival is for this turn
           if (lane == 0) {
-            S.turns[j & 3] = word;
-            mbar_arrive(&S.p_full[w]);
+            S.turns[j & 7] = word;
+            mbar_arrive(&S.p_full[j & 3]);
           }
         }
       }
@@ -367,44 +419,46 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     bool ok = true;
     auto wait = [&](uint64_t *b, uint32_t par) { ok = __all_sync(0xffffffffu, at_wait(b, par, &S.gave_up, a.status)) && ok; };
-    auto scores = [&](int w, uint32_t word) {
-      if (word & TURN_WAIT_Q) wait(&S.q_full, word & TURN_Q_PAR ? 1 : 0);
+    auto scores = [&](int b, int j, uint32_t word) {  // of turn j, to tile b
+      const int q = word & TURN_Q_SLOT ? 1 : 0;
+      if (word & TURN_WAIT_Q) wait(&S.q_full[q], word & TURN_Q_PAR ? 1 : 0);
       const int slot = word / TURN_K_SLOT & 15;
       if (word & TURN_WAIT_K) wait(&S.k_full[slot], word & TURN_K_PAR ? 1 : 0);
       if (!ok) return;
       tc_fence_after();
-      const uint64_t qd = q0 + (word & TURN_Q_TILE ? C::TILE / 16 : 0), kd = k0 + slot * (C::TILE / 16);
+      const uint64_t qd = q0 + 2 * q * (C::TILE / 16) + (word & TURN_Q_TILE ? C::TILE / 16 : 0), kd = k0 + slot * (C::TILE / 16);
 #pragma unroll
       for (int x = 0; x < DP / 16; ++x) {  // (addresses in a descriptor count 16 bytes)
         const uint32_t at = (x / 4 * (AT_KEYS * 128) + x % 4 * 32) / 16;
-        mma_f16_by(by, tm + w * 128, qd + at, kd + at, id_s, x > 0);
+        mma_f16_by(by, tm + b * 128, qd + at, kd + at, id_s, x > 0);
       }
-      mma_commit_by(by, &S.s_full[w]);
+      mma_commit_by(by, &S.s_full[j & 3]);
       if (word & TURN_FREE_K) mma_commit_by(by, &S.k_empty[slot]);
-      if (word & TURN_FREE_Q) mma_commit_by(by, &S.q_empty);
+      if (word & TURN_FREE_Q) mma_commit_by(by, &S.q_empty[q]);
     };
-    // the first turn's scores of each group, which no turn precedes (their
+    // the first turns' scores, which no turn precedes (their
     // segments are not let go of before these scores are used)
     Ahead z{};
     z.segment(S.segs, 0, tok, a.status);
     const bool some = z.count > 0;
-    for (int j = 0; ok && j < 2 && z.count; ++j) {
-      scores(j, __shfl_sync(0xffffffffu, z.word<KS>(j), 0));
-      if (j == 0) z.step(S.segs, tok, a.status);
+    for (int j = 0; ok && j < C::NB && z.count; ++j) {
+      scores(j, j, __shfl_sync(0xffffffffu, z.word<KS, QS>(j & 1), 0));
+      if (j + 1 < C::NB) z.step(S.segs, tok, a.status);
     }
-    for (int j = 0; ok && some; ++j) {
+    for (int j = 0, b = 0; ok && some; ++j, b = b + 1 == C::NB ? 0 : b + 1) {
       const int w = j & 1;
-      wait(&S.p_full[w], j >> 1 & 1);
+      wait(&S.p_full[j & 3], j >> 2 & 1);
       if (!ok) break;
-      const uint32_t word = __shfl_sync(0xffffffffu, S.turns[j & 3], 0);
+      const uint32_t word = __shfl_sync(0xffffffffu, S.turns[j & 7], 0);
       tc_fence_after();
       const int slot = word / TURN_V_SLOT & 15;
       const uint64_t vd = v0 + slot * (C::TILE / 16);
 #pragma unroll
       for (int x = 0; x < AT_KEYS / 16; ++x)
-        mma_f16_ts_by(by, tm + 256 + w * 128, tm + w * 128 + x * 8, vd + x * 2048 / 16, id_o, true);
-      if (word & TURN_SUMS) mma_commit_by(by, &S.o_full[w]);
-      if (word & TURN_SCORES) scores(w, word);
+        mma_f16_ts_by(by, tm + C::SUMS + w * DP, tm + b * 128 + x * 8, vd + x * 2048 / 16, id_o, true);
+      if (C::NB > 2) mma_commit_by(by, &S.o_full[j & 3]);
+      else if (word & TURN_SUMS) mma_commit_by(by, &S.o_full[w]);
+      if (word & TURN_SCORES) scores(b, j + C::NB, word);
       if (word & TURN_FREE_V) mma_commit_by(by, &S.v_empty[slot]);
       if (word & TURN_LAST) break;
     }
@@ -415,11 +469,14 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
   } else {
     // ------------------------------------------------------------- softmax --
     const int grp = warp >> 2, row = tid & 127;
+    constexpr int W = C::WIDE;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t t_s = tmem + lanes + grp * 128, t_o = tmem + lanes + 256 + grp * 128;
+    const uint32_t t_o = tmem + lanes + C::SUMS + grp * DP;
     const float sc = a.scale_log2;
     const int my_tok = row / a.g, my_head = row - my_tok * a.g;
-    int f = 0, turn = 0, mine = 0, ends = 0;  // tile and turn of the stretch; turns and segments of this group
+    // tile and turn of the stretch; turns of this group (the i-th is turn
+    // 2 i + group), and its segments; where the next turn's scores are
+    int f = 0, turn = 0, mine = 0, ends = 0, b = grp;
     for (int ks = 0;; ++ks) {
       const Seg &s = S.segs.get(ks, a.status);
       __syncwarp();
@@ -442,49 +499,59 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       for (int i = 0; i < count; ++i, j0 += AT_KEYS, ++f) {
         turn += two ? 2 : 1;
         if (!two && ((turn - 1) & 1) != grp) continue;
-        at_wait_warp(&S.s_full[grp], mine & 1, &S.gave_up, a.status);
+        at_wait_warp(&S.s_full[(2 * mine + grp) & 3], mine >> 1 & 1, &S.gave_up, a.status);
+        // (the products of the turn before the last, in order, so that the
+        // parity tells which)
+        if (C::NB > 2 && mine >= 2) at_wait_warp(&S.o_full[(2 * mine + grp) & 3], (mine >> 1) - 1 & 1, &S.gave_up, a.status);
         tc_fence_after();
+        // before this thread changes the sums itself, the group's products are complete
+        auto settle = [&]() {
+          if (C::NB > 2 && done) at_wait_warp(&S.o_full[(2 * mine + grp + 2) & 3], (mine - 1) >> 1 & 1, &S.gave_up, a.status);
+          tc_fence_after();
+        };
+        const uint32_t t_s = tmem + lanes + b * 128;
         // columns [lo, hi) of the tile are seen; the others' scores are
         // replaced in tensor memory too
         const int hi = is_row ? pos + 1 - j0 : 0, lo = a.window ? pos + 1 - a.window - j0 : 0;
         const bool edge = edge_of(p0 + skip, n, j0);
+        if (edge && W == 64) mask_scores(t_s, lo, hi);
         float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < AT_KEYS; c0 += 64) {
-          float x[64];
-          tmem_ld64(t_s + c0, x);
-          if (edge) {
-            const uint32_t s0 = bits(lo - c0, hi - c0), s1 = bits(lo - c0 - 32, hi - c0 - 32);
+        for (int c0 = 0; c0 < AT_KEYS; c0 += W) {
+          float x[W];
+          load_scores(t_s + c0, x);
+          if (edge && W == 32) {
+            const uint32_t see = bits(lo - c0, hi - c0);
 #pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = (c < 32 ? s0 : s1) >> (c & 31) & 1u ? x[c] : -INFINITY;
-            tmem_st64(t_s + c0, x);
+            for (int c = 0; c < W; ++c) x[c] = see >> (c & 31) & 1u ? x[c] : -INFINITY;
+            tmem_st32(t_s + c0, x);
           }
 #pragma unroll
-          for (int c = 0; c < 64; c += 8) {
+          for (int c = 0; c < W; c += 8) {
             t0 = fmaxf(t0, fmaxf(x[c], x[c + 1]));
             t1 = fmaxf(t1, fmaxf(x[c + 2], x[c + 3]));
             t2 = fmaxf(t2, fmaxf(x[c + 4], x[c + 5]));
             t3 = fmaxf(t3, fmaxf(x[c + 6], x[c + 7]));
           }
         }
-        if (edge) tmem_st_wait();
+        if (edge && W == 32) tmem_st_wait();
         const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sc;
         if (__any_sync(0xffffffffu, top > m + AT_SLACK)) {
-          // raise the maximum, and bring the sums down to it (the earlier
-          // products are complete: these scores were issued behind them)
+          // raise the maximum, and bring the sums down to it
           const float to = fmaxf(m, top), keep = ex2(m - to);
           l *= keep;
           m = to;
+          settle();
           if (done) scale_sums<DP>(t_o, keep);
         }
         const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < AT_KEYS; c0 += 64) {
-          float x[64];
-          tmem_ld64(t_s + c0, x);
+        for (int c0 = 0; c0 < AT_KEYS; c0 += W) {
+          float x[W];
+          load_scores(t_s + c0, x);
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
+          for (int c = 0; c < W; c += 4) {
             const float2 u = fma2(make_float2(x[c], x[c + 1]), sc2, m2), w = fma2(make_float2(x[c + 2], x[c + 3]), sc2, m2);
             const float2 p = make_float2(ex2(u.x), ex2(u.y)), q = make_float2(ex2(w.x), ex2(w.y));
             sum0 = add2(sum0, p);
@@ -492,7 +559,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             x[c / 2] = __uint_as_float(pack16<BF16>(p.x, p.y));
             x[c / 2 + 1] = __uint_as_float(pack16<BF16>(q.x, q.y));
           }
-          tmem_st32(t_s + c0 / 2, x);
+          if (W == 64) tmem_st32(t_s + c0 / 2, x);
+          else tmem_st16(t_s + c0 / 2, x);
         }
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
         if (edge_of(p0, n0, j0)) {
@@ -502,6 +570,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
           const int sl = f % VS;
           at_wait_warp(&S.v_seen[sl], f / VS & 1, &S.gave_up, a.status);
           if (S.odd[sl][0] | S.odd[sl][1] | S.odd[sl][2] | S.odd[sl][3]) {
+            settle();
             add_odd<DP, BF16>(vring + sl * C::TILE, S.odd[sl], lo, hi, t_o);
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.added[grp]);
@@ -511,14 +580,16 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full[grp]);
+        if (lane == 0) mbar_arrive(&S.p_full[(2 * mine + grp) & 3]);
         __syncwarp();
+        b = C::NB == 2 ? b : b ? b - 1 : 2;  // (two turns on, of three)
         ++mine;
         ++done;
       }
       // ---- the segment's end ----
       if (done) {
-        at_wait_warp(&S.o_full[grp], ends++ & 1, &S.gave_up, a.status);
+        if (C::NB > 2) at_wait_warp(&S.o_full[(2 * mine + grp + 2) & 3], (mine - 1) >> 1 & 1, &S.gave_up, a.status);
+        else at_wait_warp(&S.o_full[grp], ends++ & 1, &S.gave_up, a.status);
         tc_fence_after();
       }
       const bool whole = (s.flags & (SEG_START | SEG_END)) == (SEG_START | SEG_END);
@@ -554,7 +625,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         for (int k = 0; k < 16; ++k) o[k] *= scale;
         if (!two) {
           float p[16];
-          tmem_ld16(tmem + lanes + 256 + (1 - grp) * 128 + c, p);
+          tmem_ld16(tmem + lanes + C::SUMS + (1 - grp) * DP + c, p);
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = fmaf(p[k], other, o[k]);
         }
@@ -601,8 +672,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
 template <int DP, bool BF16>
 cudaError_t launch(const AttnArgs &a, void *ws, cudaStream_t s) {
   using C = AcCfg<DP>;
-  constexpr size_t smem = AC_HEAD + (2 + C::KS + C::VS) * C::TILE;
-  static_assert(sizeof(AcShared<C::KS, C::VS>) <= AC_HEAD, "head of a block's shared memory");
+  constexpr size_t smem = AC_HEAD + (2 * C::QS + C::KS + C::VS) * C::TILE;
+  static_assert(sizeof(AcShared<C::KS, C::VS, C::QS>) <= AC_HEAD, "head of a block's shared memory");
   static_assert(smem <= 227 * 1024, "shared memory of a block");
   static OncePerDevice once;
   cudaError_t e = once_per_device(once, []() {

@@ -5,8 +5,9 @@
 // Work is counted in tiles of 128 keys.  An item is a block of query rows
 // (tpb tokens of one request, with the query heads that share a key head)
 // and the tiles that any of its tokens sees; items follow one another by
-// request, key head and block.  The tiles of all items form one line, which
-// the launch's blocks share out evenly whatever the lengths are: a block
+// request, key head and block.  The tiles of all items form one line, on which
+// each has the length that it costs (Plan), and which the launch's blocks
+// share out evenly whatever the lengths are: a block
 // takes a stretch of the line, so it begins inside an item and ends inside
 // another.  Each such piece leaves its sums, unnormalised, in the workspace
 // (at most two a block), and a second kernel joins them in the order of the
@@ -149,22 +150,25 @@ __device__ __forceinline__ bool not_finite2(uint32_t w) {
   return (w & M) == M || (w & (M << 16)) == (M << 16);
 }
 
-constexpr int AT_ITEM = 2;
-
 // Bits [lo, hi) of a word.
 __device__ __forceinline__ uint32_t bits(int lo, int hi) {
   const uint32_t below = hi >= 32 ? 0xffffffffu : hi > 0 ? (1u << hi) - 1u : 0u;
   return lo >= 32 ? 0u : lo > 0 ? below & ~((1u << lo) - 1u) : below;
 }
 
-// Whether any of a run of 16-byte words' 16-bit floats is an infinity or NaN:
-// the largest magnitude tells.
+// Where the x-th 16-byte word that a lane takes of its key's row is: the lanes
+// of a warp, a row each, begin at different words, so that they meet in
+// different banks (which word is which does not matter to the callers).
+__device__ __forceinline__ uint32_t row_word(int x, int lane) { return x / 8 * (AT_KEYS * 128) + ((x ^ lane) & 7) * 16; }
+
+// Whether any of a key's 16-bit floats is an infinity or NaN: the largest
+// magnitude tells.
 template <bool BF16, int WORDS>
-__device__ __forceinline__ bool not_finite_row(const uint8_t *row) {
+__device__ __forceinline__ bool not_finite_row(const uint8_t *row, int lane) {
   uint32_t top = 0;
 #pragma unroll
   for (int x = 0; x < WORDS; ++x) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(row + x / 8 * (AT_KEYS * 128) + x % 8 * 16);
+    const uint4 w = *reinterpret_cast<const uint4 *>(row + row_word(x, lane));
     top = __vimax3_u16x2(top, w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
     top = __vimax3_u16x2(top, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
   }
@@ -180,13 +184,23 @@ __device__ __forceinline__ void tile_range(const Span &s, int first, int n, int 
   end = max(begin + 1, (p + n + AT_KEYS - 1) / AT_KEYS);
 }
 
+// What an item is and what it costs.
+struct Plan {
+  int tpb;   // tokens
+  int wide;  // more tokens than this, and a tile counts twice
+  int item;  // units that an item costs besides its tiles
+  __device__ __forceinline__ int shift(int n) const { return n > wide; }
+  __device__ __forceinline__ int64_t length(int begin, int end, int n) const { return ((int64_t)(end - begin) << shift(n)) + item; }
+};
+
 // Length on the line of one key head's items of a request.
-__device__ __forceinline__ int64_t request_line(const Span &s, int tpb, int window) {
+__device__ __forceinline__ int64_t request_line(const Span &s, const Plan &p, int window) {
   int64_t sum = 0;
-  for (int f = 0; f < s.n; f += tpb) {
+  for (int f = 0; f < s.n; f += p.tpb) {
+    const int n = min(p.tpb, s.n - f);
     int b, e;
-    tile_range(s, f, min(tpb, s.n - f), window, b, e);
-    sum += e - b + AT_ITEM;
+    tile_range(s, f, n, window, b, e);
+    sum += p.length(b, e, n);
   }
   return sum;
 }
@@ -223,15 +237,15 @@ __device__ __forceinline__ RawSpan first_request(const AttnArgs &a) {
 // By all THREADS threads; *out is in shared memory and valid after the
 // caller's next barrier.
 template <int THREADS>
-__device__ __forceinline__ void find_start(const AttnArgs &a, const RawSpan &raw0, int tpb, Start *out, int64_t *part) {
+__device__ __forceinline__ void find_start(const AttnArgs &a, const RawSpan &raw0, const Plan &p, Start *out, int64_t *part) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.R + THREADS - 1) / THREADS, r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
   bool bad = false;
   Span sp0 = request_span(raw0, a.T, a.max_new, a.max_seq, bad);
-  const int64_t line0 = r0 < r1 ? request_line(sp0, tpb, a.window) : 0;
+  const int64_t line0 = r0 < r1 ? request_line(sp0, p, a.window) : 0;
   int64_t mine = line0;
   for (int r = r0 + 1; r < r1; ++r)
-    mine += request_line(request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad), tpb, a.window);
+    mine += request_line(request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad), p, a.window);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -248,9 +262,9 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, const RawSpan &raw
   }
   total *= a.G;
   before *= a.G;
-  // no stretch is shorter than an item's overhead and a tile: with little to
-  // do the first blocks have a tile each
-  const int64_t c = blockIdx.x, blocks = gridDim.x, least = AT_ITEM + 1;
+  // no stretch is shorter than an item's overhead and a unit: with little to
+  // do the first blocks have a tile each (or two that count once)
+  const int64_t c = blockIdx.x, blocks = gridDim.x, least = p.item + 1;
   int64_t s = min(c * least, total), e = min((c + 1) * least, total);
   if (total >= blocks * least) {
     int64_t rest;
@@ -266,7 +280,7 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, const RawSpan &raw
     for (int r = r0; r < r1; ++r) {
       if (r > r0) {
         sp = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
-        line = request_line(sp, tpb, a.window);
+        line = request_line(sp, p, a.window);
       }
       if (off >= line * a.G) {
         off -= line * a.G;
@@ -277,9 +291,11 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, const RawSpan &raw
       out->h = (int)divide(off, line, off);
       int b = 0, t0, t1;
       for (;; ++b) {
-        tile_range(sp, b * tpb, min(tpb, sp.n - b * tpb), a.window, t0, t1);
-        if (off < t1 - t0 + AT_ITEM) break;
-        off -= t1 - t0 + AT_ITEM;
+        const int n = min(p.tpb, sp.n - b * p.tpb);
+        tile_range(sp, b * p.tpb, n, a.window, t0, t1);
+        const int64_t len = p.length(t0, t1, n);
+        if (off < len) break;
+        off -= len;
       }
       out->b = b;
       out->at = (int)off;
@@ -291,46 +307,52 @@ __device__ __forceinline__ void find_start(const AttnArgs &a, const RawSpan &raw
 
 // The segments of a block's stretch, in order: runs of tiles of one item
 // (none of them empty).  An item's places on the line are its overhead and
-// then its tiles.
+// then its tiles'; a tile is the block's whose stretch has its first place.
 struct Segments {
+  Plan p;
   int r, h, b, at, begin, end, tile, count, index;
   int64_t left;
   Span sp;
   // of the segment: its first token in the request, its tokens
   int first, n;
 
-  __device__ __forceinline__ void init(const AttnArgs &a, int tpb, const Start &s) {
+  __device__ __forceinline__ void init(const AttnArgs &a, const Plan &plan, const Start &s) {
+    p = plan;
     r = s.r; h = s.h; b = s.b; at = s.at; left = s.left;
     index = 0;
     count = 0;
     if (left > 0) {
       sp = s.sp;
-      item(a, tpb);
-      if (!count) advance(a, tpb);
+      item(a);
+      if (!count) advance(a);
     }
   }
   // The tiles of the current item from place `at` on, as far as the stretch goes.
-  __device__ __forceinline__ void item(const AttnArgs &a, int tpb) {
-    first = b * tpb;
-    n = min(tpb, sp.n - first);
+  __device__ __forceinline__ void item(const AttnArgs &a) {
+    first = b * p.tpb;
+    n = min(p.tpb, sp.n - first);
     tile_range(sp, first, n, a.window, begin, end);
-    tile = begin + max(0, at - AT_ITEM);
-    const int64_t stop = min(at + left, (int64_t)(end - begin + AT_ITEM));
-    count = (int)max(stop - AT_ITEM, (int64_t)0) - (tile - begin);
+    auto tiles = [&](int64_t place) {  // that begin before it
+      const int sh = p.shift(n);
+      return (int)((max(place - p.item, (int64_t)0) + sh) >> sh);
+    };
+    const int done = tiles(at);
+    tile = begin + done;
+    count = tiles(min(at + left, p.length(begin, end, n))) - done;
   }
   __device__ __forceinline__ bool has_start() const { return tile == begin; }
   __device__ __forceinline__ bool has_end() const { return tile + count == end; }
-  __device__ __forceinline__ void next(const AttnArgs &a, int tpb) {
+  __device__ __forceinline__ void next(const AttnArgs &a) {
     ++index;
-    advance(a, tpb);
+    advance(a);
   }
-  __device__ __forceinline__ void advance(const AttnArgs &a, int tpb) {
+  __device__ __forceinline__ void advance(const AttnArgs &a) {
     do {
-      left -= end - begin + AT_ITEM - at;
+      left -= p.length(begin, end, n) - at;
       at = 0;
       count = 0;
       if (left <= 0) return;
-      if (++b * tpb >= sp.n) {
+      if (++b * (int64_t)p.tpb >= sp.n) {
         b = 0;
         if (++h == a.G) {
           h = 0;
@@ -344,7 +366,7 @@ struct Segments {
           } while (sp.n == 0);
         }
       }
-      item(a, tpb);
+      item(a);
     } while (!count);
   }
 };
@@ -420,7 +442,8 @@ inline Pieces pieces_of(void *ws, int blocks, int rows, int dp) {
 // are many (one request's long sequence under one key head is shared by all
 // blocks) the eight warps of a block share a row's pieces, and then their
 // results (152 pieces of 100,000 keys: 77 us with a warp a row, 15 us so,
-// from a cold cache).
+// from a cold cache; with 2 to 4 pieces a row a shared form's warps idle: 17
+// requests of 3 to 666 tokens 76 us with a warp a row, 114 shared).
 constexpr int JOIN_WARPS = 8, JOIN_FEW = 8, JOIN_BLOCKS = 32;
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) attention_join_kernel(const AttnArgs a, const Pieces p, int rows, int tok) {

@@ -117,7 +117,9 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v) {
 // sums the row chunk by chunk (a warp a chunk), the blocks exchange their
 // totals through shared memory, and the block that the drawn number falls
 // into finds the chunk and the entry in it.  Bound by reading one row of the
-// target and one of the draft.
+// target and one of the draft, after the loads of the drafts' probabilities
+// that say which (96 requests, 100,003 entries of 32 bits: 16 us with the rows
+// in L2, 20 from HBM, 3.4 TB/s; one request of 32,768 entries 5.8 us).
 template <bool BF16>
 __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const VerifyArgs a) {
   extern __shared__ int64_t chunk[];
