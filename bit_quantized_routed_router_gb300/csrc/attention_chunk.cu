@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       const int sl = f % KS;
       if (lane == 0 && f >= KS && !at_wait(&S.k_empty[sl], (f / KS & 1) ^ 1, &S.gave_up, a.status)) ok = false;
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      now.copy<DP>(a, kring + sl * C::TILE, &tm_k, head, rows, &S.k_full[sl], bad);
+      now.copy<DP, false>(a, kring + sl * C::TILE, &tm_k, nullptr, head, rows, &S.k_full[sl], bad);
       now = later;
     }
     S.segs.put(segs, s, false, &S.gave_up, a.status);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
       const int sl = f % VS;
       if (lane == 0 && f >= VS && !at_wait(&S.v_empty[sl], (f / VS & 1) ^ 1, &S.gave_up, a.status)) ok = false;
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (ok) now.copy<DP>(a, vring + sl * C::TILE, &tm_v, head, rows, &S.v_full[sl], bad);
+      if (ok) now.copy<DP, false>(a, vring + sl * C::TILE, &tm_v, nullptr, head, rows, &S.v_full[sl], bad);
       else break;
       now = later;
     }

@@ -69,7 +69,7 @@ struct AdShared {
 template <int N, int DP, bool BF16>
 __global__ void __launch_bounds__(AD_THREADS, 1)
     attention_decode_kernel(const AttnArgs a, const Pieces pieces, const __grid_constant__ CUtensorMap tm_q,
-                            const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, int rows) {
+                            const __grid_constant__ KvMaps tm_k, const __grid_constant__ KvMaps tm_v, int rows) {
   using C = AdCfg<N, DP>;
   constexpr int SLOTS = C::SLOTS;
   constexpr Plan PLAN = {1 << 20, 1 << 20, AD_ITEM};  // one block of tokens a request
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
     if (i == 0) mbar_init(&S.drain, 1), S.gave_up = 0;
     fence_mbar_init();
   } else if (tid == 64) {
-    const CUtensorMap *maps[3] = {&tm_q, &tm_k, &tm_v};
+    const CUtensorMap *maps[3] = {&tm_q, &tm_k.one, &tm_v.one};
     for (int i = 0; i < 3; ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
   }
   if (tid == 0) {
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
   if (warp == AD_KEYS || warp == AD_VALUES) {
     // ------------------------------------------------------------ copies --
     const bool keys = warp == AD_KEYS;
-    const CUtensorMap *map = keys ? &tm_k : &tm_v;
+    const KvMaps *maps = keys ? &tm_k : &tm_v;
     bool ok = true, bad = false;
     int segs = 0, f = 0, i = 0;  // segments begun, tile of the stretch, of the segment
     TileRuns now, later;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
       const int sl = f % SLOTS;
       if (lane == 0 && f >= SLOTS && !at_wait(&S.empty[!keys][sl], ((f / SLOTS) & 1) ^ 1, &S.gave_up, a.status)) ok = false;
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      now.copy<DP>(a, (keys ? kring : vring) + sl * C::TILE, map, head, rows, &S.full[!keys][sl], bad);
+      now.copy<DP, true>(a, (keys ? kring : vring) + sl * C::TILE, &maps->one, &maps->two, head, rows, &S.full[!keys][sl], bad);
       now = later;
     }
     if (bad) flag(a.status, ST_PAGING);
@@ -476,8 +476,9 @@ cudaError_t launch(const AttnArgs &a, void *ws, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   const int blocks = device_sms(), rows = piece_rows(a.page);
-  CUtensorMap tq, tk, tv;
-  if (!make_q_map(&tq, a, N / a.g, BF16) || !make_kv_map(&tk, a.k, a, rows, BF16) || !make_kv_map(&tv, a.v, a, rows, BF16))
+  CUtensorMap tq;
+  KvMaps tk, tv;
+  if (!make_q_map(&tq, a, N / a.g, BF16) || !make_kv_maps(&tk, a.k, a, rows, BF16) || !make_kv_maps(&tv, a.v, a, rows, BF16))
     return cudaErrorInvalidValue;
   const Pieces p = pieces_of(ws, blocks, N, DP);
   attention_decode_kernel<N, DP, BF16><<<blocks, AD_THREADS, smem, s>>>(a, p, tq, tk, tv, rows);

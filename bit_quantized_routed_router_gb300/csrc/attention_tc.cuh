@@ -586,6 +586,25 @@ inline int piece_rows(int page) {
   return b;
 }
 
+// Maps of keys or values: for boxes of `rows` rows, and of twice as many for
+// two runs that lie together in a page.  Only pages of an odd number of 8-row
+// runs use the second: an SM's copies run at about 50 cycles a box, which
+// boxes of 8 rows do not keep up with memory at and boxes of 16 do (64
+// requests of 200 to 8200 keys, 8 key heads of 128: 191 us with pages of 24 in
+// single runs, 177 in pairs, 177 with pages of 16).  The chunk kernel takes
+// single runs: it reads less, and the code for pairs slows it (17 requests of 3
+// to 666 tokens: 82 us without, 93 with).
+struct KvMaps {
+  CUtensorMap one, two;
+};
+constexpr int AT_PAIR_ROWS = 8;
+inline bool make_kv_maps(KvMaps *m, const void *base, const AttnArgs &a, int rows, bool bf16) {
+  if (!make_kv_map(&m->one, base, a, rows, bf16)) return false;
+  if (rows == AT_PAIR_ROWS && a.page > rows) return make_kv_map(&m->two, base, a, 2 * rows, bf16);
+  m->two = m->one;
+  return true;
+}
+
 // The copies of one tile's keys (and later its values): lane i < 128 / rows
 // has the i-th run of rows, its page and its first row there.  Runs that no
 // token of the segment sees, and pages that are none, are filled with zeros.
@@ -608,15 +627,22 @@ struct TileRuns {
   __device__ __forceinline__ void find(const AttnArgs &a, const Segments &s, int tile, int rows) {
     find(a, s.r, s.sp.pos0 + s.first, s.n, tile, rows);
   }
-  template <int DP>
-  __device__ __forceinline__ void copy(const AttnArgs &a, uint8_t *slot, const CUtensorMap *map, int head, int rows,
+  template <int DP, bool PAIRS>
+  __device__ __forceinline__ void copy(const AttnArgs &a, uint8_t *slot, const CUtensorMap *one, const CUtensorMap *two, int head, int rows,
                                        uint64_t *full, bool &bad) const {
     const int lane = threadIdx.x & 31;
     if (lane == 0) mbar_arrive_expect_tx(full, AT_KEYS * DP * 2);
     __syncwarp();
-    if (lane * rows < AT_KEYS) {
-      const bool there = sees && page >= 0 && page < a.n_pages;
-      bad = bad || (sees && !there);
+    const bool there = sees && page >= 0 && page < a.n_pages;
+    bad = bad || (sees && !there);
+    bool pair = false, paired = false;  // takes the next lane's run along; is taken along
+    if (PAIRS && rows == AT_PAIR_ROWS && a.page > AT_PAIR_ROWS) {
+      const bool next = __shfl_down_sync(0xffffffffu, there, 1);  // (past the tile's last run: not there)
+      pair = there && next && !(row & AT_PAIR_ROWS) && row + 2 * AT_PAIR_ROWS <= a.page;
+      paired = __shfl_up_sync(0xffffffffu, pair, 1) && lane > 0;
+    }
+    if (lane * rows < AT_KEYS && !paired) {
+      const CUtensorMap *map = pair ? two : one;
 #pragma unroll
       for (int x = 0; x < DP; x += 64)
         tma_load_4d(slot + x / 64 * (AT_KEYS * 128) + lane * rows * 128, map, x, there ? row : 0, head, there ? page : -1, full);
