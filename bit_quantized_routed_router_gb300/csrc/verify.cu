@@ -118,8 +118,8 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v) {
 // totals through shared memory, and the block that the drawn number falls
 // into finds the chunk and the entry in it.  Bound by reading one row of the
 // target and one of the draft, after the loads of the drafts' probabilities
-// that say which (96 requests, 100,003 entries of 32 bits: 16 us with the rows
-// in L2, 20 from HBM, 3.4 TB/s; one request of 32,768 entries 5.8 us).
+// that say which (96 requests, 100,003 entries of 32 bits: 15 us with the rows
+// in L2, 19 from HBM, 3.6 TB/s; one request of 32,768 entries 5.8 us).
 template <bool BF16>
 __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const VerifyArgs a) {
   extern __shared__ int64_t chunk[];
@@ -296,11 +296,13 @@ int ds_moe_verify_drafts(const void *target, int64_t target_stride, const void *
   if (!a.status) return fail(err, errlen, DS_ERR_CUDA, "no CUDA device");
   const int chunks = (vocab + VD_CHUNK - 1) / VD_CHUNK, sms = device_sms();
   if (!sms) return fail(err, errlen, DS_ERR_CUDA, "no CUDA device");
-  // as many blocks a request as one wave of blocks has room for (96 requests
-  // of 100,003 entries: 27 us with 8, in two waves, 19 us with 4), and no more
-  // than there are chunks for their warps
+  // as many blocks a request as one wave of blocks has room for, and no more
+  // than there are chunks for their warps (100,003 entries, rows in L2: 96
+  // requests 27 us with 8, in two waves, 15.4 with 6, 16.5 with 4; from HBM 200
+  // requests 42 us with 2, 46 with 3, so odd sizes are left out at the low end)
   int ranks = VD_CLUSTER;
-  while (ranks > 1 && ((int64_t)n_requests * ranks > sms * VD_RESIDENT || chunks <= VD_WARPS * (ranks / 2))) ranks /= 2;
+  auto fewer = [](int n) { return n > 4 ? n - 1 : n / 2; };
+  while (ranks > 1 && ((int64_t)n_requests * ranks > sms * VD_RESIDENT || chunks <= VD_WARPS * fewer(ranks))) ranks = fewer(ranks);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)n_requests * ranks);
   cfg.blockDim = dim3(VD_THREADS);
