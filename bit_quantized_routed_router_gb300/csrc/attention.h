@@ -25,10 +25,13 @@ struct AttnArgs {
 };
 
 // Query rows a key head up to which the decode kernel serves: its work goes
-// with the rows, the chunk kernel's with tiles of 128 of them (64 requests of
-// 200 to 8200 keys, 4 key heads: at 32 rows decode 185 us for head_dim 128 and
-// 136 for 64; at 40 a 64-column form of it, which is therefore left out, 284
-// and 243, chunk 213 and 214; at 56 299 and 255, and 217 and 215).
+// with the rows, the chunk kernel's with tiles of 128 of them.  64 requests of
+// 200 to 8200 keys, 4 key heads, at 16, 24 and 32 rows: decode 95, 100 and
+// 100 us for head_dim 128, chunk 102, 103 and 104; for 64 decode 61, 72 and 72,
+// chunk 62, 62 and 63, but with few requests decode is ahead there as well (24
+// rows: 4 requests of 1000 to 3000 keys 14 and 16, 3 of 60,000 to 90,000 100
+// and 105).  A 64-column form of it was behind at 40 rows (284 us for 128,
+// chunk 213, with twice the heads) and is left out.
 constexpr int64_t AD_MAX_ROWS = 32;
 size_t attention_decode_workspace(int64_t rows, int blocks);
 cudaError_t launch_attention_decode(const AttnArgs &a, bool bf16, void *ws, cudaStream_t s);
