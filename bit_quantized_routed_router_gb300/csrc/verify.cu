@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const V
   extern __shared__ int64_t chunk[];
   __shared__ int64_t totals[2][VD_CLUSTER], part[VD_WARPS];
   const cg::cluster_group cluster = cg::this_cluster();
+  cluster.barrier_arrive();  // this block has begun: its shared memory can be written to
   const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
   const int r = blockIdx.x / ranks, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c0 = a.cu[r], c1 = a.cu[r + 1];
@@ -195,6 +196,9 @@ __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const V
       }
       if (lane == 0) part[warp] = sum;
       __syncthreads();
+      // the others have begun too (that they are scheduled together does not
+      // say so; the loads since the arrival hide the wait)
+      if (turn == 0) cluster.barrier_wait();
       if (tid < ranks) {  // this block's total to every block
         int64_t s = 0;
 #pragma unroll
@@ -257,6 +261,8 @@ __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const V
         }
       }
     }
+  } else {
+    cluster.barrier_wait();
   }
   if (bad) flag(a.status, ST_DRAFT);
 }

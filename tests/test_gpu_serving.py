@@ -556,3 +556,28 @@ def test_verify_keeps_the_targets_distribution():
     count = np.bincount(out[:, 0], minlength=V)
     pe = p.double().numpy()
     assert np.all(np.abs(count - n * pe) <= 5 * np.sqrt(n * pe * (1 - pe)))
+
+
+def test_verify_beside_other_work():
+    """Blocks of a cluster that begin when another stream's kernels leave them room exchange their totals all the same."""
+    n, V, mx = 70, 20011, 4
+    p, q, tokens, cu, ua, us = draws(11, n, 0, 4, V)
+    want = ref.verify(p.numpy(), q.numpy(), tokens, cu, ua, us, mx)
+    dev = lambda a, t: torch.as_tensor(a).to(t).cuda()  # noqa: E731
+    args = (p.cuda(), q.cuda(), dev(tokens, torch.int32), dev(cu, torch.int32), dev(ua, torch.float32), dev(us, torch.float32))
+    turns = 24
+    out = torch.full((turns, n, mx), 99, dtype=torch.int32, device="cuda")
+    kept = torch.full((turns, n), 99, dtype=torch.int32, device="cuda")
+    m = torch.randn(2048, 2048, device="cuda").bfloat16()
+    busy, own = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(turns):
+        with torch.cuda.stream(busy):
+            for _ in range(3):
+                m @ m
+        with torch.cuda.stream(own):
+            ds.verify_drafts(*args, out[i], kept[i])
+    torch.cuda.synchronize()
+    ds.sync_status()
+    for i in range(turns):
+        assert np.array_equal(out[i].cpu().numpy(), want[0]) and np.array_equal(kept[i].cpu().numpy(), want[1])
