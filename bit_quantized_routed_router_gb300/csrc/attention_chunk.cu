@@ -167,6 +167,7 @@ __device__ __noinline__ void scale_sums(uint32_t t_o, float by) {
     for (int k = 0; k < 16; ++k) o[k] *= by;
     tmem_st16(t_o + c, o);
   }
+  tmem_st_wait();  // (add_odd may load them next)
 }
 
 // Adds to a row's sums the values of a tile that are not finite and that the
@@ -189,6 +190,7 @@ __device__ __noinline__ void add_odd(const uint8_t *vt, const uint32_t *odd, int
       }
       tmem_st16(t_o + c, o);
     }
+    tmem_st_wait();  // the next key's loads are of the same columns
   }
 }
 

@@ -151,6 +151,29 @@ def test_attention_later_tokens_have_no_influence(what, new, D):
             assert bool(torch.isfinite(out[new - 1, :, 9:]).all()) and bool(torch.isfinite(out[new - 1, :, :3]).all())
 
 
+@pytest.mark.parametrize("new", [8, 100, 150, 300])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_attention_many_infinities_in_a_tile(new, D, dtype):
+    """Several values that are not finite in one tile, each seen by some rows only, where the maxima rise from tile to
+    tile: rows that do not see them keep their sums, the others get what the formula gives."""
+    ctx = 120
+    c = growing(ref.Case([ctx, 40], [new, 3], 8, 2, D, 16, dtype=dtype), 1)
+    for i, (at, what) in enumerate(((1, math.inf), (2, math.inf), (3, -math.inf), (new // 2, math.nan), (new - 4, math.inf),
+                                    (new - 3, -math.inf), (new - 1, math.nan))):
+        c.values[0][ctx + at, :, 5 * i: 5 * i + 7] = what  # (neighbours share elements)
+    c.put()
+    out, lse = attend(c)
+    ds.sync_status()
+    want, wlse, mag = c.reference()
+    tol, ltol = c.tolerances(want, mag, True)
+    got, fin = out.cpu().double(), torch.isfinite(want)
+    assert not bool(fin.all()) and torch.equal(torch.isfinite(got), fin)
+    assert torch.equal(got[~fin].nan_to_num(7.0), want[~fin].nan_to_num(7.0))
+    assert bool(((got - want).abs() <= tol)[fin].all())
+    assert bool(((lse.cpu().double() - wlse).abs() <= ltol + 2.0 ** -24 * wlse.abs()).all())
+
+
 @pytest.mark.parametrize("new", [1, 3, 150])
 def test_attention_keys_before_the_window_have_no_influence(new):
     c = ref.Case([400], [new], 4, 2, 128, 16, window=90)
