@@ -553,10 +553,12 @@ def paged_attention(shape: AttentionShape, cache: KVCache, block_table, q, cu_ne
     table, width, stride = _table(block_table, R)
     if out.size(0) < T:
         raise ValueError("out has too few rows")
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace: need a dense device tensor")
     room = workspace.numel() * workspace.element_size()
     _call(lib().ds_moe_paged_attention, shape._c, cache._c, table, width, stride, qp, qs, T, _array(cu_new, "cu_new", 32, R + 1),
           _array(seq_lens, "seq_lens", 32), R, max_new, op, os_,
-          None if lse is None else _array(lse, "lse", 32, T * shape.n_head), _array(workspace, "workspace", _type(workspace)[0]), room,
+          None if lse is None else _array(lse, "lse", 32, T * shape.n_head), workspace.data_ptr(), room,
           _stream(stream))
 
 

@@ -121,3 +121,40 @@ def test_binding_refuses_host_tensors_and_wrong_types(L):
         ds.KVCache(torch.zeros(2, 16, 8, 128, dtype=torch.bfloat16), torch.zeros(2, 16, 8, 128, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         ds.verify_drafts(torch.zeros(2, 9), None, i, i, i, i, i.view(2, 2), i)
+
+
+class OnDevice(torch.Tensor):
+    """A host tensor that says it is on the device: arguments that the binding turns down before it calls."""
+    is_cuda = True
+
+
+def on_device(*shape, dtype=torch.int32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice)
+
+
+@pytest.fixture
+def calls(L, monkeypatch):
+    """What the binding would hand to the library, which is not called."""
+    seen = []
+    monkeypatch.setattr(ds, "_call", lambda fn, *args: seen.append(fn.__name__))
+    return seen
+
+
+def attend(**kw):
+    bf16 = torch.bfloat16
+    a = dict(table=on_device(2, 3), q=on_device(3, 4, 64, dtype=bf16), cu=on_device(3), seq=on_device(2),
+             out=on_device(3, 4, 64, dtype=bf16), workspace=on_device(1 << 20, dtype=torch.uint8), lse=None) | kw
+    cache = ds.KVCache(on_device(4, 16, 2, 64, dtype=bf16), on_device(4, 16, 2, 64, dtype=bf16))
+    ds.paged_attention(ds.AttentionShape(4, 2, 64, 16), cache, a["table"], a["q"], a["cu"], a["seq"], 2, a["out"], a["workspace"],
+                       lse=a["lse"], stream=0)
+
+
+def test_binding_refuses_a_workspace_on_the_host(calls):
+    for bad in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1 << 17, dtype=torch.float64),
+                on_device(1 << 20, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError, match="workspace"):
+            attend(workspace=bad)
+    assert not calls
+    attend()
+    attend(workspace=on_device(1 << 17, dtype=torch.float64))
+    assert calls == ["ds_moe_paged_attention"] * 2
