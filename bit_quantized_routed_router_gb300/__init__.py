@@ -488,15 +488,19 @@ def _half(t, shape, name):
         raise ValueError(f"{name}: need a device tensor of the shape's type")
 
 
-def _array(t, name, bits, n=0):
-    """Address of a dense device array of `bits`-bit elements, n of them at least."""
-    if _type(t)[0] != bits or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{name}: need a dense device tensor of {bits}-bit elements, {n} or more")
+_INT32, _INT64, _FLOAT32 = (32, None), (64, None), (32, DS_F32)  # _type's of arrays
+_NAMES = {_INT32: "int32", _INT64: "int64", _FLOAT32: "fp32"}
+
+
+def _array(t, name, kind, n=0):
+    """Address of a dense device array of that type, of n elements at least."""
+    if _type(t) != kind or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: need a dense device tensor of {_NAMES[kind]}, {n} elements or more")
     return t.data_ptr()
 
 
 def _table(t, rows):
-    if t.dim() != 2 or _type(t)[0] != 32 or (t.size(1) > 1 and t.stride(1) != 1) or t.size(0) < rows:
+    if t.dim() != 2 or _type(t) != _INT32 or (t.size(1) > 1 and t.stride(1) != 1) or t.size(0) < rows:
         raise ValueError(f"block_table: need a device int32 tensor [{rows} requests][pages], rows dense")
     return t.data_ptr(), t.size(1), t.stride(0)
 
@@ -507,10 +511,10 @@ def page_map(context_lens, new_lens, free_pages, block_table, page_size: int, sl
     block_table, slots, positions, cu_new, seq_lens and n_taken are written."""
     R, cap = context_lens.numel(), slots.numel()
     table, width, stride = _table(block_table, R)
-    _call(lib().ds_moe_page_map, _array(context_lens, "context_lens", 32), _array(new_lens, "new_lens", 32, R), R,
-          page_size, _array(free_pages, "free_pages", 32), free_pages.numel(), table, width, stride,
-          _array(slots, "slots", 64), _array(positions, "positions", 32, cap), cap,
-          _array(cu_new, "cu_new", 32, R + 1), _array(seq_lens, "seq_lens", 32, R), _array(n_taken, "n_taken", 32, 1),
+    _call(lib().ds_moe_page_map, _array(context_lens, "context_lens", _INT32), _array(new_lens, "new_lens", _INT32, R), R,
+          page_size, _array(free_pages, "free_pages", _INT32), free_pages.numel(), table, width, stride,
+          _array(slots, "slots", _INT64), _array(positions, "positions", _INT32, cap), cap,
+          _array(cu_new, "cu_new", _INT32, R + 1), _array(seq_lens, "seq_lens", _INT32, R), _array(n_taken, "n_taken", _INT32, 1),
           _stream(stream))
 
 
@@ -524,7 +528,7 @@ def kv_append(shape: AttentionShape, cache: KVCache, k_new, v_new, slots, stream
             or not v_new.is_cuda):
         raise ValueError("k_new and v_new: device tensors [T][n_head_kv][head_dim] of the same strides, the last axis dense")
     T = k_new.size(0)
-    _call(lib().ds_moe_kv_append, shape._c, cache._c, k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], _array(slots, "slots", 64, T), T, _stream(stream))
+    _call(lib().ds_moe_kv_append, shape._c, cache._c, k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], _array(slots, "slots", _INT64, T), T, _stream(stream))
 
 
 def attention_workspace_bytes(shape: AttentionShape, n_requests: int, T: int, max_new: int) -> int:
@@ -556,9 +560,9 @@ def paged_attention(shape: AttentionShape, cache: KVCache, block_table, q, cu_ne
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace: need a dense device tensor")
     room = workspace.numel() * workspace.element_size()
-    _call(lib().ds_moe_paged_attention, shape._c, cache._c, table, width, stride, qp, qs, T, _array(cu_new, "cu_new", 32, R + 1),
-          _array(seq_lens, "seq_lens", 32), R, max_new, op, os_,
-          None if lse is None else _array(lse, "lse", 32, T * shape.n_head), workspace.data_ptr(), room,
+    _call(lib().ds_moe_paged_attention, shape._c, cache._c, table, width, stride, qp, qs, T, _array(cu_new, "cu_new", _INT32, R + 1),
+          _array(seq_lens, "seq_lens", _INT32), R, max_new, op, os_,
+          None if lse is None else _array(lse, "lse", _FLOAT32, T * shape.n_head), workspace.data_ptr(), room,
           _stream(stream))
 
 
@@ -585,7 +589,7 @@ def verify_drafts(target, draft, tokens, cu_new, u_accept, u_sample, out_tokens,
     if out_tokens.dim() != 2 or out_tokens.size(0) != R:
         raise ValueError("out_tokens: need [requests][max_new]")
     _call(lib().ds_moe_verify_drafts, target.data_ptr(), strides[0], _ptr(draft), 0 if draft is None else draft.stride(0),
-          kind, T, V, _array(tokens, "tokens", 32, T),
-          _array(cu_new, "cu_new", 32, R + 1), R, out_tokens.size(1), _array(u_accept, "u_accept", 32, T),
-          _array(u_sample, "u_sample", 32, R), _array(out_tokens, "out_tokens", 32), _array(n_accepted, "n_accepted", 32),
+          kind, T, V, _array(tokens, "tokens", _INT32, T),
+          _array(cu_new, "cu_new", _INT32, R + 1), R, out_tokens.size(1), _array(u_accept, "u_accept", _FLOAT32, T),
+          _array(u_sample, "u_sample", _FLOAT32, R), _array(out_tokens, "out_tokens", _INT32), _array(n_accepted, "n_accepted", _INT32),
           _stream(stream))

@@ -158,3 +158,39 @@ def test_binding_refuses_a_workspace_on_the_host(calls):
     attend()
     attend(workspace=on_device(1 << 17, dtype=torch.float64))
     assert calls == ["ds_moe_paged_attention"] * 2
+
+
+# the binding's calls, with arguments that it lets through
+F32, I64, BF16 = torch.float32, torch.int64, torch.bfloat16
+CALLS = {
+    "page_map": (lambda a: ds.page_map(*a.values(), stream=0),
+                 dict(context_lens=on_device(2), new_lens=on_device(2), free_pages=on_device(9), block_table=on_device(2, 3), page_size=16,
+                      slots=on_device(8, dtype=I64), positions=on_device(8), cu_new=on_device(3), seq_lens=on_device(2), n_taken=on_device(1))),
+    "kv_append": (lambda a: ds.kv_append(ds.AttentionShape(4, 2, 64, 16), ds.KVCache(a["k"], a["v"]), a["k_new"], a["v_new"], a["slots"], stream=0),
+                  dict(k=on_device(4, 16, 2, 64, dtype=BF16), v=on_device(4, 16, 2, 64, dtype=BF16), k_new=on_device(3, 2, 64, dtype=BF16),
+                       v_new=on_device(3, 2, 64, dtype=BF16), slots=on_device(3, dtype=I64))),
+    "paged_attention": (lambda a: attend(**a),
+                        dict(table=on_device(2, 3), q=on_device(3, 4, 64, dtype=BF16), cu=on_device(3), seq=on_device(2),
+                             out=on_device(3, 4, 64, dtype=BF16), lse=on_device(3, 4, dtype=F32))),
+    "verify_drafts": (lambda a: ds.verify_drafts(*a.values(), stream=0),
+                      dict(target=on_device(5, 9, dtype=F32), draft=on_device(5, 9, dtype=F32), tokens=on_device(5), cu_new=on_device(3),
+                           u_accept=on_device(5, dtype=F32), u_sample=on_device(2, dtype=F32), out_tokens=on_device(2, 3),
+                           n_accepted=on_device(2))),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_binding_refuses_other_types_and_host_tensors_in_every_place(calls, name):
+    call, args = CALLS[name]
+    call(args)
+    assert calls == ["ds_moe_" + name]
+    for key, t in args.items():
+        if not torch.is_tensor(t):
+            continue
+        plain = t.as_subclass(torch.Tensor)
+        # floats for whole numbers of the same width and the other way round, another width, and the host
+        others = {torch.int32: (F32, I64), I64: (torch.float64, torch.int32), F32: (torch.int32, torch.float64), BF16: (torch.float16, F32)}
+        for bad in [plain] + [plain.to(d).as_subclass(OnDevice) for d in others[t.dtype]]:
+            with pytest.raises(ValueError):
+                call(args | {key: bad})
+    assert len(calls) == 1
