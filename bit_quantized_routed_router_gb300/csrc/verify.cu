@@ -30,6 +30,7 @@ struct VerifyArgs {
   const int32_t *tokens, *cu;
   const float *u_accept, *u_sample;
   int32_t *out, *n_accepted;
+  float unit;  // 2^22 / 2^k: see weights()
   unsigned *status;
 };
 
@@ -61,13 +62,15 @@ __device__ __forceinline__ void load8(const void *base, int64_t row, int x0, int
 // the target's p and the draft's q (zeros where it is not to count), or none
 // at the draft `sure`.
 //
-// A weight is a whole number of 2^-44 units, hi * 2^22 + lo.  With q held to
-// at most p the difference is s plus an exact error e (Dekker's fast two-sum);
+// A weight is a whole number of 2^-(44 - k) units, hi * 2^22 + lo, with `unit`
+// = 2^(22 - k): k is 0 for vocabularies below 2^19 and goes up to 4 at 2^22,
+// so that a vocabulary of ones adds up to less than 2^63.  With q held to at
+// most p the difference is s plus an exact error e (Dekker's fast two-sum);
 // adding 1.5 * 2^23 rounds to whole numbers, which are the low bits of the
 // sum.  Sums of such numbers are exact, so no order of adding changes the
 // token that is drawn; fp64 adds would be slower than HBM here.
-__device__ __forceinline__ int64_t weights(float pv[8], float qv[8], int sure, int x0, int step, int64_t each[8], bool &bad) {
-  constexpr float MAGIC = 12582912.f, UNIT = 4194304.f;  // 1.5 * 2^23, 2^22
+__device__ __forceinline__ int64_t weights(float pv[8], float qv[8], float unit, int sure, int x0, int step, int64_t each[8], bool &bad) {
+  constexpr float MAGIC = 12582912.f, LOW = 4194304.f;  // 1.5 * 2^23, 2^22
   constexpr uint32_t MAGIC_BITS = 0x4B400000u;
   uint32_t top = 0;
 #pragma unroll
@@ -87,9 +90,9 @@ __device__ __forceinline__ int64_t weights(float pv[8], float qv[8], int sure, i
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float y = fminf(pv[i], qv[i]), s = pv[i] - y, e = (pv[i] - s) - y;
-    const float t = fmaf(s, UNIT, MAGIC);
-    const float rem = fmaf(e, UNIT, fmaf(s, UNIT, -(t - MAGIC)));
-    const uint32_t hi = __float_as_uint(t) - MAGIC_BITS, lo = __float_as_uint(fmaf(rem, UNIT, MAGIC)) - MAGIC_BITS;
+    const float t = fmaf(s, unit, MAGIC);
+    const float rem = fmaf(e, unit, fmaf(s, unit, -(t - MAGIC)));
+    const uint32_t hi = __float_as_uint(t) - MAGIC_BITS, lo = __float_as_uint(fmaf(rem, LOW, MAGIC)) - MAGIC_BITS;
     if (each) each[i] = ((int64_t)(int)hi << 22) + (int)lo;
     hs += hi;
     ls += lo;
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const V
 #pragma unroll
         for (int i = 0; i < 8; ++i) pv[i] = pn[i], qv[i] = qn[i];
         if (c + VD_WARPS < mine) load(c + VD_WARPS, pn, qn);  // (the next chunk's loads, before this one's arithmetic)
-        const int64_t s = warp_sum64(weights(pv, qv, sure, (first + c) * VD_CHUNK + lane, 32, nullptr, bad));
+        const int64_t s = warp_sum64(weights(pv, qv, a.unit, sure, (first + c) * VD_CHUNK + lane, 32, nullptr, bad));
         if (lane == 0) chunk[c] = s;
         sum += s;
       }
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const V
         float pv[8], qv[8];
         load8<BF16, false>(a.p, prow, x0, 1, a.V, pv);
         load8<BF16, false>(q, qrow, x0, 1, a.V, qv);
-        const int64_t v = weights(pv, qv, sure, x0, 1, each, none), incl = warp_scan64(v);
+        const int64_t v = weights(pv, qv, a.unit, sure, x0, 1, each, none), incl = warp_scan64(v);
         const unsigned pass = __ballot_sync(0xffffffffu, before + incl > thr);
         if (pass && lane == __ffs(pass) - 1) {
           int64_t run = before + incl - v;
@@ -297,8 +300,10 @@ int ds_moe_verify_drafts(const void *target, int64_t target_stride, const void *
   if (!aligned(target, el) || !aligned(draft, el) || !aligned(tokens, 4) || !aligned(cu_new, 4) ||
       !aligned(u_accept, 4) || !aligned(u_sample, 4) || !aligned(out_tokens, 4) || !aligned(n_accepted, 4))
     return fail(err, errlen, DS_ERR_INVALID_ARG, "arrays must be aligned to their elements");
+  int k = 0;
+  while (vocab >> (19 + k)) ++k;
   VerifyArgs a{target, draft, target_stride, draft_stride, (int)T, vocab, n_requests, max_new, tokens, cu_new, u_accept,
-               u_sample, out_tokens, n_accepted, status_word()};
+               u_sample, out_tokens, n_accepted, (float)(1 << (22 - k)), status_word()};
   if (!a.status) return fail(err, errlen, DS_ERR_CUDA, "no CUDA device");
   const int chunks = (vocab + VD_CHUNK - 1) / VD_CHUNK, sms = device_sms();
   if (!sms) return fail(err, errlen, DS_ERR_CUDA, "no CUDA device");

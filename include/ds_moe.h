@@ -481,24 +481,28 @@ int ds_moe_paged_attention(const ds_moe_attn_shape *shape, const ds_moe_kv_cache
  * drafts; row cu_new[r] + i of target and draft is the distribution of the
  * token behind its i-th, so draft i (from 1) is checked against row
  * cu_new[r] + i - 1.
- *   target  [T][vocab], dtype DS_F32 or DS_BF16, rows target_stride elements
- *           apart: the model's probabilities (any scale: a row is normalised
- *           by its sum when it is sampled from)
+ *   target  [T][vocab] (vocab up to 2^22), dtype DS_F32 or DS_BF16, rows
+ *           target_stride elements apart: the model's probabilities, each in
+ *           [0, 1].  A row need not add up to 1 where it is sampled from (it
+ *           is normalised by its sum); drafts are judged by its entries as
+ *           they are
  *   draft   the same for the drafter (rows of drafts only are read), or NULL:
  *           the drafter was sure of each draft
  *   u_accept [T] fp32 (entry of draft i: cu_new[r] + i - 1), u_sample
  *           [n_requests] fp32, in [0, 1)
  * Draft x at row i is kept while u_accept * draft(x) < target(x), exactly.
  * At the first that is not, one token is drawn from max(target - draft, 0)
- * (from target where that is zero throughout); when all were kept, from the
+ * (from target where nothing is left); when all were kept, from the
  * target row behind the last.  Drawn is the least token whose cumulative sum
- * exceeds u_sample times the total; the sums are whole numbers of 2^-44, so
- * they do not depend on any order.
+ * exceeds u_sample times the total.  What is summed are entries (or
+ * differences) rounded to whole numbers of 2^-44, of 2^-43 for vocabularies
+ * from 2^19 up, and so on to 2^-40 for 2^22: the sums are exact, so they do not
+ * depend on any order, and less than half a unit counts as nothing.
  *   out_tokens [n_requests][max_new] int32: the drafts kept, the token drawn,
  *           then -1;  n_accepted [n_requests] int32: drafts kept
  * A request without new tokens gives -1s and 0.  Reported: a draft outside
- * the vocabulary (it is not kept), a row that is sampled from and has no
- * positive probability (token -1), probabilities that are NaN, negative or
+ * the vocabulary (it is not kept), a row that is sampled from and has nothing
+ * that counts (token -1), probabilities that are NaN, negative or
  * above 1 in a row that is sampled from (NaN and negative count as 0, others
  * as 1), lengths beyond T or max_new (dropped). */
 int ds_moe_verify_drafts(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride,

@@ -604,3 +604,56 @@ def test_verify_beside_other_work():
     ds.sync_status()
     for i in range(turns):
         assert np.array_equal(out[i].cpu().numpy(), want[0]) and np.array_equal(kept[i].cpu().numpy(), want[1])
+
+
+def drawn(w, u):
+    """The least entry whose cumulative weight exceeds u times the total: whole numbers throughout."""
+    total, m = sum(w), int(float(np.float32(u)) * 2 ** 48)  # (u here is a multiple of 2^-48)
+    run = 0
+    for x, v in enumerate(w):
+        run += v
+        if run << 48 > m * total:
+            return x
+    return -1
+
+
+@pytest.mark.parametrize("V", [262145, 524287, 524288, 600000, 1048577, 1200000, 1 << 22])
+@pytest.mark.parametrize("drafted", [True, False])
+def test_verify_large_rows_that_are_not_normalised(V, drafted):
+    """Entries of 1 throughout add up to the vocabulary's size; u times that is exact here, and so is the entry drawn."""
+    us = [0.0, 0.25, 0.3, 0.625, float(np.nextafter(np.float32(1), np.float32(0)))]
+    p = torch.ones(1, V).cuda()
+    for u in us:
+        want = int(float(np.float32(u)) * V)
+        out, n = run_verify(p, None, [0], [0, 1], [0.0], [u], 1)
+        assert n[0] == 0 and out[0].tolist() == [want]
+    # a refused draft, entry 3, of which the target has nothing: the others weigh the same
+    p = p.repeat(2, 1)
+    p[:, 3] = 0
+    q = torch.full((2, V), 0.25).cuda() if drafted else None
+    for u in us:
+        out, n = run_verify(p, q, [0, 3], [0, 2], [0.0, 0.0], [u], 2)
+        at = int(float(np.float32(u)) * (V - 1))
+        assert n[0] == 0 and out[0].tolist() == [at + (at >= 3), -1]
+
+
+def test_verify_small_entries():
+    """Entries that are whole multiples of 2^-44 count as they are, whatever their sum; less than half of it is none."""
+    rng = np.random.default_rng(3)
+    w = rng.integers(0, 9, 3000)
+    for u in (0.0, 0.125, 0.7, float(np.nextafter(np.float32(1), np.float32(0)))):
+        p = torch.tensor(w * 2.0 ** -44, dtype=torch.float32)[None]
+        out, n = run_verify(p, None, [0], [0, 1], [0.0], [u], 1)
+        assert n[0] == 0 and out[0, 0] == drawn(w.tolist(), u)
+    p = torch.full((1, 500), 2.0 ** -46)
+    p[0, 77] = 0.75 * 2.0 ** -44
+    assert run_verify(p, None, [0], [0, 1], [0.0], [0.9], 1)[0][0, 0] == 77
+    p[0, 77] = 0
+    out, n = run_verify(p, None, [0], [0, 1], [0.0], [0.9], 1, bad=True)
+    assert n[0] == 0 and out[0, 0] == -1
+    # nothing that counts is left above the draft: the target itself is drawn from
+    p = torch.tensor([[2.0 ** -30, 0.5, 0.0, 0.5]] * 2)
+    q = p.clone()
+    q[:, 0] -= 2.0 ** -50
+    out, n = run_verify(p, q, [0, 2], [0, 2], [0.0, 0.0], [0.75], 2)
+    assert n[0] == 0 and out[0].tolist() == [3, -1]
