@@ -116,6 +116,16 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v) {
   return v;
 }
 
+// Whole part of u * total, exactly, for 0 <= u < 1: u is m 2^(e - 150), the
+// product 87 bits at most.
+__device__ __forceinline__ int64_t whole_part(float u, int64_t total) {
+  const uint32_t w = __float_as_uint(u) & 0x7FFFFFFFu, e = w >> 23;  // (below 127)
+  const uint64_t m = e ? (w & 0x7FFFFFu) | 0x800000u : w;
+  const int down = 150 - (int)(e ? e : 1);  // 24 at least
+  const uint64_t lo = m * (uint64_t)total, hi = __umul64hi(m, (uint64_t)total);
+  return (int64_t)(down < 64 ? hi << (64 - down) | lo >> down : down < 128 ? hi >> (down - 64) : 0);
+}
+
 // A cluster of blocks a request, each with a part of the vocabulary: pass 1
 // sums the row chunk by chunk (a warp a chunk), the blocks exchange their
 // totals through shared memory, and the block that the drawn number falls
@@ -228,8 +238,7 @@ __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const V
       // the entry drawn is the least whose cumulative weight exceeds u * total
       const float u = a.u_sample[r];
       if (!(u >= 0.f && u < 1.f)) bad = true;
-      int64_t thr = u >= 1.f ? total - 1 : u >= 0.f ? (int64_t)((double)u * (double)total) : 0;
-      thr = min(thr, total - 1);
+      const int64_t thr = u >= 1.f ? total - 1 : u >= 0.f ? whole_part(u, total) : 0;
       if (before <= thr && thr < before + own) {  // it is in this block's entries
         int at = 0;
         for (int b = 0; b < mine; b += 32) {

@@ -657,3 +657,23 @@ def test_verify_small_entries():
     q[:, 0] -= 2.0 ** -50
     out, n = run_verify(p, q, [0, 2], [0, 2], [0.0, 0.0], [0.75], 2)
     assert n[0] == 0 and out[0].tolist() == [3, -1]
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_verify_draws_by_exact_products(seed):
+    """u times the total lies just below a whole number, which a cumulative sum reaches: that entry is drawn, not the next."""
+    rng, found = random.Random(seed), 0
+    while found < 5:
+        total, m = rng.randrange(1 << 43, 1 << 44) | 1, rng.randrange(1 << 23, 1 << 24) | 1
+        below = -(m * total) % (1 << 24)  # u = m 2^-24: what is missing to the whole number above, in 2^-24
+        if not 0 < below < 1 << 12:
+            continue
+        found += 1
+        reach = (m * total >> 24) + 1
+        parts = lambda n: [n >> 20 << 20, n & (1 << 20) - 1]  # noqa: E731  (24 bits each)
+        w = parts(reach) + parts(total - reach)
+        assert sum(w) == total and all(v > 0 for v in w)
+        p = torch.tensor([v * 2.0 ** -44 for v in w])[None]
+        assert [int(v * 2.0 ** 44) for v in p[0].tolist()] == w
+        out, n = run_verify(p, None, [0], [0, 1], [0.0], [m * 2.0 ** -24], 1)
+        assert n[0] == 0 and out[0, 0] == drawn(w, m * 2.0 ** -24) == 1
