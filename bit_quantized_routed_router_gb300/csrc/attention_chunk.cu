@@ -538,9 +538,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         }
         if (edge && W == 32) tmem_st_wait();
         const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sc;
-        if (__any_sync(0xffffffffu, top > m + AT_SLACK)) {
+        if (__any_sync(0xffffffffu, top > m + (AT_SLACK + AT_LIFT<BF16>))) {
           // raise the maximum, and bring the sums down to it
-          const float to = fmaxf(m, top), keep = ex2(m - to);
+          const float to = fmaxf(m, top - AT_LIFT<BF16>), keep = ex2(m - to);
           l *= keep;
           m = to;
           settle();

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           float top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < N; c += 2) top = fmaxf(top, fmaxf(x[c], x[c + 1]));
-          if (again || (done && !bar_or(1 + grp, 128, top > AT_SLACK))) break;  // (a segment's first tile sets them)
+          if (again || (done && !bar_or(1 + grp, 128, top > AT_SLACK + AT_LIFT<BF16>))) break;  // (a segment's first tile sets them)
           // raise the maxima to the tile's, and bring the sums down to them
           settle();
           float v[N];
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1)
           if (key < N) {
             const float was = S.ref[grp][key];
             const float to = fmaxf(fmaxf(fmaxf(S.top[grp][0][key], S.top[grp][1][key]),
-                                         fmaxf(S.top[grp][2][key], S.top[grp][3][key])), was);
+                                         fmaxf(S.top[grp][2][key], S.top[grp][3][key])) - AT_LIFT<BF16>, was);
             S.ref[grp][key] = to;
             S.factor[grp][key] = ex2(was - to);
           }

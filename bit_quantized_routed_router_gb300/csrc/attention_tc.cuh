@@ -30,8 +30,14 @@ constexpr uint64_t AT_LIMIT_NS = 2000000000ull;
 constexpr float AT_LN2 = 0.69314718055994531f;
 // A running maximum is raised only when a score exceeds it by this much (in
 // powers of two): probabilities then stay below 2^8, which costs nothing in a
-// 16-bit float, and accumulators are rarely rescaled.
+// bf16, and accumulators are rarely rescaled.
 constexpr float AT_SLACK = 8.f;
+// What is kept as an fp16 row's maximum is this much less than it, so that
+// probabilities go from 2^7 (2^15 with the slack) down: fp16's steps end at
+// 2^-24, and a long flat tail would lose its weight there.  2^-32 of the
+// largest is as much as one can be off by then.
+template <bool BF16>
+constexpr float AT_LIFT = BF16 ? 0.f : 7.f;
 constexpr float AT_NONE = -FLT_MAX;  // maximum of no scores
 
 // Bounded wait; once one has run out, every wait gives up at once.  (What

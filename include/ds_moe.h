@@ -464,8 +464,9 @@ int ds_moe_attention_workspace_bytes(const ds_moe_attn_shape *shape, int32_t n_r
  * their values hold (infinities and NaN included).  A token that sees no key
  * (its sequence is shorter than its chunk) has out 0 and lse -infinity.
  * Rows of out beyond cu_new[n_requests] are not written.  Sums, maxima and
- * products are held in fp32; the probabilities are rounded to dtype for the
- * second product (at most half a unit in the last place each).  A page id
+ * products are held in fp32; on the tensor cores the probabilities are rounded
+ * to dtype for the second product (off by at most half a unit in the last place
+ * each; in fp16, those below 2^-21 of the row's largest by 2^-32 of it).  A page id
  * outside the cache counts as a page of zeros, and is reported.
  * T == 0 or n_requests == 0 is a no-op.  Workspace: 256-byte aligned, scratch.
  * The result does not depend on the order in which blocks run. */

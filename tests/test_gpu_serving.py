@@ -677,3 +677,32 @@ def test_verify_draws_by_exact_products(seed):
         assert [int(v * 2.0 ** 44) for v in p[0].tolist()] == w
         out, n = run_verify(p, None, [0], [0, 1], [0.0], [m * 2.0 ** -24], 1)
         assert n[0] == 0 and out[0, 0] == drawn(w, m * 2.0 ** -24) == 1
+
+
+@pytest.mark.parametrize("new", [1, 8, 30, 70])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_attention_flat_tail_below_a_sharp_key(new, D, dtype):
+    """Two keys that take nearly all of the probability and have no values; what the others, 2^-25.5 of them each, add up
+    to is the output.  In fp16 a probability is off by 2^-11 of itself, or of 2^-21 of the row's largest where it is
+    below that (fp16's steps end at 2^-24, and the largest is taken as 2^7 or more): half of 2^-31."""
+    c = ref.Case([1500 - new] * 76, [new] * 76, 8, 2, D, 16, dtype=dtype, seed=new)
+    c.q_cpu = torch.zeros_like(c.q_cpu)
+    c.q_cpu[..., 0] = 16.0
+    for k, v in zip(c.keys, c.values):
+        k *= 0.01
+        k[[5, 133]] = 0
+        k[[5, 133], :, 0] = 25.5 * math.log(2) * math.sqrt(D) / 16
+        v += 1
+        v[[5, 133]] = 0
+    c.put()
+    out, lse = attend(c)
+    ds.sync_status()
+    assert c.path != ds.ATTN_GENERIC
+    want, wlse, mag = c.reference()
+    tol, ltol = c.tolerances(want, mag, True)
+    if dtype == "f16":
+        sums = torch.stack([v.double().abs().sum(0) for v in c.values])  # [requests][key heads][D]
+        tol = tol + 2.0 ** -32 * sums.repeat_interleave(4, 1).repeat_interleave(new, 0)
+    assert bool(((out.cpu().double() - want).abs() <= tol).all())
+    assert bool(((lse.cpu().double() - wlse).abs() <= ltol + 2.0 ** -24 * wlse.abs()).all())
