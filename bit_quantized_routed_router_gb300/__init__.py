@@ -567,8 +567,9 @@ def paged_attention(shape: AttentionShape, cache: KVCache, block_table, q, cu_ne
 
 
 def attention_path(shape: AttentionShape, cache: KVCache, q, max_new: int) -> int:
-    """Which kernels paged_attention runs (an ATTN_* value)."""
-    rc = lib().ds_moe_attention_path(shape._c, cache._c, q.data_ptr(), q.stride(0), max_new)
+    """Which kernels paged_attention runs (an ATTN_* value) with a table of one column or more."""
+    stride = q.stride(0) if q.size(0) > 1 else shape.n_head * shape.head_dim  # (a lone token's is not used)
+    rc = lib().ds_moe_attention_path(shape._c, cache._c, q.data_ptr(), stride, max_new)
     if rc < 0:
         raise DsMoeError(rc, "shape, cache or max_new rejected")
     return rc

@@ -511,8 +511,11 @@ int ds_moe_verify_drafts(const void *target, int64_t target_stride, const void *
                          int32_t n_requests, int32_t max_new, const float *u_accept, const float *u_sample,
                          int32_t *out_tokens, int32_t *n_accepted, void *stream, char *err, size_t errlen);
 
-/* Which kernels ds_moe_paged_attention runs (host call; nothing is
- * launched): one of the DS_ATTN_* values, or a negative ds_status. */
+/* Which kernels ds_moe_paged_attention runs with a table of one column or
+ * more (without columns there are no keys, and the call is DS_ATTN_GENERIC's;
+ * host call; nothing is launched): one of the DS_ATTN_* values, or a negative
+ * ds_status.  q_stride: as for several tokens; the stride of a single one is
+ * not used, so n_head * head_dim stands for it. */
 enum {
   DS_ATTN_GENERIC = 0, /* any strides, page and head sizes: CUDA cores        */
   DS_ATTN_DECODE = 1,  /* up to 32 query rows (max_new * n_head / n_head_kv)

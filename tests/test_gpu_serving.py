@@ -706,3 +706,18 @@ def test_attention_flat_tail_below_a_sharp_key(new, D, dtype):
         tol = tol + 2.0 ** -32 * sums.repeat_interleave(4, 1).repeat_interleave(new, 0)
     assert bool(((out.cpu().double() - want).abs() <= tol).all())
     assert bool(((lse.cpu().double() - wlse).abs() <= ltol + 2.0 ** -24 * wlse.abs()).all())
+
+
+def test_attention_path_of_a_single_token():
+    """A lone token's stride is not used, so it does not keep the call from the tensor cores; q given the same way to both."""
+    c = ref.Case([20], [1], 8, 2, 64, 16).put()
+    room = torch.empty(2, 8 * 64 + 3, dtype=c.dt, device="cuda")
+    q, q2 = (room.as_strided((n, 8, 64), (8 * 64 + 3, 64, 1)) for n in (1, 2))
+    assert q.stride(0) % 8
+    sh, cache = shape_of(c), ds.KVCache(c.k, c.v)
+    assert ds.attention_path(sh, cache, q, 1) == ds.ATTN_DECODE
+    assert ds.attention_path(sh, cache, q2, 1) == ds.ATTN_GENERIC
+    q.copy_(c.q)
+    out, _ = attend(c)
+    c.q = q
+    assert torch.equal(attend(c)[0], out)
