@@ -111,19 +111,9 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t addr, uint32_t block)
 // f16_idesc bits for an A or B operand in that layout.
 constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
 
-// D += A B with A in tensor memory (two 16-bit elements a column).
-__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
-}
-
-// The same three by a whole warp, of which the lane with `by` issues: the
-// operands are then the warp's (uniform registers), where a thread that has
-// branched off alone has to move each of them there for every product.
+// mma_f16 and mma_commit by a whole warp, of which the lane with `by` issues:
+// the operands are then the warp's (uniform registers), where a thread that
+// has branched off alone has to move each of them there for every product.
 __device__ __forceinline__ void mma_f16_by(uint32_t by, uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t"
@@ -133,6 +123,7 @@ __device__ __forceinline__ void mma_f16_by(uint32_t by, uint32_t tmem_d, uint64_
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(by)
       : "memory");
 }
+// The same with A in tensor memory (two 16-bit elements a column).
 __device__ __forceinline__ void mma_f16_ts_by(uint32_t by, uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc,
                                               bool accumulate) {
   asm volatile(
