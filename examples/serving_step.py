@@ -85,7 +85,8 @@ def run(steps=4, requests=3, drafts=3, prompt=40, check=True):
         q, k, v = qkv[:, : m.heads], qkv[:, m.heads: m.heads + m.kv], qkv[:, m.heads + m.kv:]
         ds.kv_append(m.shape, cache, k, v, slots)
         out = torch.empty(T, m.heads, m.dim, dtype=torch.bfloat16, device=dev)
-        ds.paged_attention(m.shape, cache, table, q, cu, seq, max_new, out, workspace)
+        # (the step's own largest number of new tokens, not the prompts': drafts then take the kernel for few rows)
+        ds.paged_attention(m.shape, cache, table, q, cu, seq, max(len(f) for f in fed), out, workspace)
         x = (x + out.flatten(1) @ m.back).contiguous()
         y = torch.empty(T, m.D, dtype=torch.float32, device=dev)
         normed = torch.nn.functional.rms_norm(x.float(), (m.D,)).bfloat16()

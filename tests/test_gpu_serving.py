@@ -721,3 +721,21 @@ def test_attention_path_of_a_single_token():
     out, _ = attend(c)
     c.q = q
     assert torch.equal(attend(c)[0], out)
+
+
+def test_example_takes_the_decode_kernel_behind_the_prompts(monkeypatch):
+    import importlib.util
+    import os
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serving_step.py")
+    spec = importlib.util.spec_from_file_location("serving_step", at)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    paths, attention = [], ds.paged_attention
+
+    def watched(shape, cache, table, q, cu, seq, max_new, *args, **kw):
+        paths.append(ds.attention_path(shape, cache, q, max_new))
+        return attention(shape, cache, table, q, cu, seq, max_new, *args, **kw)
+
+    monkeypatch.setattr(ds, "paged_attention", watched)
+    example.run(steps=3)
+    assert paths == [ds.ATTN_CHUNK, ds.ATTN_DECODE, ds.ATTN_DECODE]
