@@ -404,7 +404,13 @@ int ds_moe_sync_status(void *stream, char *err, size_t errlen);
  * so); a page beyond table_width or beyond n_free is none (table entry -1,
  * where there is one), and the slots of its tokens are -1, as are those in a
  * held page whose entry is negative.  The inputs are not changed (but for
- * the table's new entries), so that the same call again gives the same. */
+ * the table's new entries), so that the same call again gives the same; no
+ * output may share memory with an input.  In a captured graph the addresses,
+ * n_requests, n_free, table_width and max_tokens are the capture's; the
+ * lengths and the ids are read at each replay.  free_pages is not consumed:
+ * before the next step the caller drops its first *n_taken ids, on the device
+ * where a graph replays (ids[(i + *n_taken) % n_free], say), and sees to it
+ * that no id in use is among those that the step can come to. */
 int ds_moe_page_map(const int32_t *context_lens, const int32_t *new_lens, int32_t n_requests, int32_t page_size,
                     const int32_t *free_pages, int32_t n_free, int32_t *block_table, int32_t table_width,
                     int64_t table_stride, int64_t *slots, int32_t *positions, int32_t max_tokens, int32_t *cu_new,

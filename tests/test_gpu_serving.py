@@ -739,3 +739,74 @@ def test_example_takes_the_decode_kernel_behind_the_prompts(monkeypatch):
     monkeypatch.setattr(ds, "paged_attention", watched)
     example.run(steps=3)
     assert paths == [ds.ATTN_CHUNK, ds.ATTN_DECODE, ds.ATTN_DECODE]
+
+
+@pytest.mark.parametrize("max_new,path", [(8, ds.ATTN_DECODE), (40, ds.ATTN_CHUNK)])
+def test_a_captured_step_serves_other_lengths(max_new, path):
+    """page_map, kv_append, paged_attention and verify_drafts in one graph, with the lengths and the list of free pages
+    moved on by it on the device: replayed with other lengths, each step is the eager one's."""
+    R_, H, G, D, page, cap, V, width = 3, 8, 2, 64, 16, 3 * max_new, 501, 12
+    rng, g = random.Random(max_new), torch.Generator().manual_seed(max_new)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    n_pages = R_ * width + 5
+    ids = list(range(n_pages))
+    rng.shuffle(ids)
+    free, table = torch.tensor(ids, **i32), torch.full((R_, width), -1, **i32)
+    context, new = torch.zeros(R_, **i32), torch.zeros(R_, **i32)
+    slots, positions = torch.empty(cap, dtype=torch.int64, device="cuda"), torch.empty(cap, **i32)
+    cu, seq, taken = torch.empty(R_ + 1, **i32), torch.empty(R_, **i32), torch.empty(1, **i32)
+    sh = ds.AttentionShape(H, G, D, page)
+    cache = ds.KVCache(*(torch.full((n_pages, page, G, D), math.nan, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+    q = torch.zeros(cap, H, D, dtype=torch.bfloat16, device="cuda")
+    kn, vn = (torch.zeros(cap, G, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    out, ws = torch.zeros_like(q), torch.empty(ds.attention_workspace_bytes(sh, R_, cap, max_new), dtype=torch.uint8, device="cuda")
+    p, d, ua, us = (torch.zeros(*s, device="cuda") for s in ((cap, V), (cap, V), (cap,), (R_,)))
+    tokens, drawn_, kept = torch.zeros(cap, **i32), torch.empty(R_, max_new, **i32), torch.empty(R_, **i32)
+    turn = torch.arange(n_pages, device="cuda")
+    assert ds.attention_path(sh, cache, q, max_new) == path
+
+    def step():
+        ds.page_map(context, new, free, table, page, slots, positions, cu, seq, taken)
+        ds.kv_append(sh, cache, kn, vn, slots)
+        ds.paged_attention(sh, cache, table, q, cu, seq, max_new, out, ws)
+        ds.verify_drafts(p, d, tokens, cu, ua, us, drawn_, kept)
+        context.copy_(seq)
+        free.copy_(free[(turn + taken) % n_pages])  # the pages taken go behind the others
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()  # (no new tokens: a step that changes nothing)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    ctx, host_table, host_free = [0] * R_, torch.full((R_, width), -1, dtype=torch.int32), list(ids)
+    keys, values = [torch.zeros(0, G, D) for _ in range(R_)], [torch.zeros(0, G, D) for _ in range(R_)]
+    most = [max_new, 1, max_new // 2]
+    for lens in ([max_new, 1, 5], [1, 1, 1], [0, 7, 2], [0, 0, 0], most, [3, 0, max_new]):
+        T = sum(lens)
+        a = [torch.randn(cap, n, D, generator=g).bfloat16() for n in (H, G, G)]
+        pp, qq, tok, _, aa, uu = draws(T + 1, 1, cap, cap, V)
+        uu = torch.rand(R_, generator=g).numpy()
+        for t, v in ((q, a[0]), (kn, a[1]), (vn, a[2]), (p, pp), (d, qq), (tokens, torch.as_tensor(tok)), (ua, torch.as_tensor(aa)),
+                     (us, torch.as_tensor(uu)), (new, torch.tensor(lens))):
+            t.copy_(v)
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        ds.sync_status()
+        w_slots, w_pos, w_cu, w_seq, w_taken, bad = ref.page_map(ctx, lens, page, host_free, host_table, cap)
+        assert not bad and torch.equal(table.cpu(), host_table)
+        assert (slots.tolist(), positions.tolist(), cu.tolist(), seq.tolist(), int(taken)) == (w_slots, w_pos, w_cu, w_seq, w_taken)
+        host_free = host_free[w_taken:] + host_free[:w_taken]
+        for r in range(R_):
+            at = slice(w_cu[r], w_cu[r + 1])
+            keys[r], values[r] = torch.cat([keys[r], a[1][at].float()]), torch.cat([values[r], a[2][at].float()])
+        c = ref.Case(ctx, lens, H, G, D, page, seq=w_seq)
+        c.keys, c.values, c.q_cpu, c.path = keys, values, a[0][:T], path
+        if T:
+            check(c, out[:T], None)
+        assert bool((out[T:] == 7.0).all())
+        want = ref.verify(pp.numpy(), qq.numpy(), tok, w_cu, aa, uu, max_new)
+        assert np.array_equal(drawn_.cpu().numpy(), want[0]) and np.array_equal(kept.cpu().numpy(), want[1])
+        ctx = w_seq
