@@ -151,7 +151,7 @@ def test_attention_later_tokens_have_no_influence(what, new, D):
             assert bool(torch.isfinite(out[new - 1, :, 9:]).all()) and bool(torch.isfinite(out[new - 1, :, :3]).all())
 
 
-@pytest.mark.parametrize("new", [8, 100, 150, 300])
+@pytest.mark.parametrize("new", [8, 20, 100, 150, 300])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_attention_many_infinities_in_a_tile(new, D, dtype):
@@ -810,3 +810,38 @@ def test_a_captured_step_serves_other_lengths(max_new, path):
         want = ref.verify(pp.numpy(), qq.numpy(), tok, w_cu, aa, uu, max_new)
         assert np.array_equal(drawn_.cpu().numpy(), want[0]) and np.array_equal(kept.cpu().numpy(), want[1])
         ctx = w_seq
+
+
+@pytest.mark.parametrize("new", [3, 8, 20, 150])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_attention_infinities_that_leave_the_window(new, D, dtype):
+    """Values that are not finite, before the first new token and among them: rows whose window has passed them, or that
+    come before them, keep their sums."""
+    ctx, window = 400, 90
+    c = ref.Case([ctx, 40], [new, 3], 8, 2, D, 16, dtype=dtype, window=window, qscale=0.5)
+    first = ctx + 1 - window
+    for i, (at, what) in enumerate(((first - 1, math.nan), (first, math.inf), (first + 1, -math.inf), (first + new // 2, math.nan),
+                                    (ctx, math.inf), (ctx + new // 2, -math.inf), (ctx + new - 1, math.nan))):
+        c.values[0][at, :, 5 * i: 5 * i + 7] = what
+    c.put()
+    out, lse = attend(c)
+    ds.sync_status()
+    want, wlse, mag = c.reference()
+    tol, ltol = c.tolerances(want, mag, True)
+    got, fin = out.cpu().double(), torch.isfinite(want)
+    assert not bool(fin.all()) and torch.equal(torch.isfinite(got), fin)
+    assert torch.equal(got[~fin].nan_to_num(7.0), want[~fin].nan_to_num(7.0))
+    assert bool(((got - want).abs() <= tol)[fin].all())
+    assert bool(((lse.cpu().double() - wlse).abs() <= ltol + 2.0 ** -24 * wlse.abs()).all())
+
+
+@pytest.mark.parametrize("new_hi,D", [(1, 128), (4, 64), (12, 64), (12, 128)])
+def test_attention_more_requests_than_threads(new_hi, D):
+    """Every thread of a block then takes several requests, some without new tokens, and most items are of one tile."""
+    rng = random.Random(new_hi)
+    n = 1100
+    c = ref.Case(ref.lengths(rng, n, 0, 150), ref.lengths(rng, n, 0, new_hi), 8, 2, D, 8).put()
+    out, lse = attend(c)
+    ds.sync_status()
+    check(c, out, lse)
