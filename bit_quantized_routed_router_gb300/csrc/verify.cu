@@ -129,10 +129,12 @@ __device__ __forceinline__ int64_t whole_part(float u, int64_t total) {
 // A cluster of blocks a request, each with a part of the vocabulary: pass 1
 // sums the row chunk by chunk (a warp a chunk), the blocks exchange their
 // totals through shared memory, and the block that the drawn number falls
-// into finds the chunk and the entry in it.  Bound by reading one row of the
-// target and one of the draft, after the loads of the drafts' probabilities
-// that say which (96 requests, 100,003 entries of 32 bits: 15 us with the rows
-// in L2, 19 from HBM, 3.6 TB/s; one request of 32,768 entries 5.8 us).
+// into finds the chunk and the entry in it.  Bound by the dependent loads that
+// say which rows are read (lengths, drafts, their probabilities), and then by
+// the instructions an entry takes rather than by its bytes: 96 requests of
+// 100,003 entries of 32 bits, rows in L2, 15 us with a draft row and 15.5 without
+// one, 17 and 16 us with 16-bit entries; 20 us from HBM, 3.4 TB/s; one request of
+// 32,768 entries 6.2 us.
 template <bool BF16>
 __global__ void __launch_bounds__(VD_THREADS, VD_RESIDENT) verify_kernel(const VerifyArgs a) {
   extern __shared__ int64_t chunk[];
