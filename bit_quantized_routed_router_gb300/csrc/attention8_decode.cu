@@ -19,7 +19,10 @@
 // A key's scale multiplies its scores, in the row of the tile that its thread
 // has; a value's scale is its logarithm added to the score: the running maximum is then
 // that of weight times scale, whatever blocks' scales are to one another, and the sum of
-// the weights alone takes each with 1 / scale.
+// the weights alone takes each with 1 / scale.  There a key may count whose weight times
+// scale is far below the maximum: exponentials are kept another 2^22 higher (A8_MORE), so
+// that where scales are 2^120 apart weights go down to 2^-35 of the largest, and 2^30 of
+// them add up to less than 2^127; sums are brought to another maximum in two steps.
 //
 // A step is KP tiles of 128 keys, two for up to 8 query rows and one for more:
 // what each warp does once a step (waits, barriers, addresses, page ids) costs as
@@ -48,7 +51,8 @@ namespace {
 
 constexpr int A8_THREADS = 384;
 constexpr int A8_MMA = 8, A8_KEYS = 9, A8_VALUES = 10, A8_QUERIES = 11;
-constexpr float A8_LIFT = AT_LIFT<false>;
+constexpr float A8_MORE = 22.f, A8_MORE_BY = 0x1p22f, A8_LESS_BY = 0x1p-22f;
+constexpr float A8_LIFT = AT_LIFT<false> + A8_MORE;
 constexpr int A8_READERS = 10;  // warps that read the segments that the keys' warp publishes
 constexpr int A8_QSCALES = 8;  // segments whose query rows' factors are kept
 
@@ -78,7 +82,7 @@ struct A8Shared {
   uint64_t q_full[2], q_empty[2], s_full[AHEAD], p_full[2], o_full[2], drain;
   alignas(16) float query[A8_QSCALES][R];  // what a segment's rows were divided by
   alignas(16) float ref[2][R];
-  alignas(16) float factor[2][R];
+  float2 factor[2][R];  // (one factor, in two parts)
   alignas(16) float2 weight[R];
   int64_t place[R];
   float top[2][4][32];
@@ -672,18 +676,21 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
             const float to = fmaxf(fmaxf(fmaxf(S.top[grp][0][key], S.top[grp][1][key]),
                                          fmaxf(S.top[grp][2][key], S.top[grp][3][key])) - A8_LIFT, was);
             S.ref[grp][key] = to;
-            S.factor[grp][key] = ex2(was - to);
+            S.factor[grp][key] = ex2_parts(was - to);
           }
           warps_bar(1 + grp, 128);
           if (done) {
 #pragma unroll
-            for (int c = 0; c < R; ++c) l[c] *= S.factor[grp][c];
+            for (int c = 0; c < R; ++c) l[c] = l[c] * S.factor[grp][c].x * S.factor[grp][c].y;
 #pragma unroll 1
             for (int c0 = 0; c0 < NP; c0 += 16) {
               float o[16];
               tmem_ld16(t_o + c0, o);
 #pragma unroll
-              for (int c = 0; c < 16; ++c) o[c] *= S.factor[grp][(c0 + c) & (R - 1)];
+              for (int c = 0; c < 16; ++c) {
+                const float2 f = S.factor[grp][(c0 + c) & (R - 1)];
+                o[c] *= f.x * f.y;
+              }
               tmem_st16(t_o + c0, o);
             }
             tmem_st_wait();
@@ -698,7 +705,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
             const float2 w = fma2(make_float2(p0, p1), make_float2(per[t], per[t]), make_float2(l[c], l[c + 1]));
             l[c] = w.x;
             l[c + 1] = w.y;
-            x[t][c / 2] = __uint_as_float(pack16<false>(p0, p1));
+            const float2 q = mul2(make_float2(p0, p1), make_float2(A8_LESS_BY, A8_LESS_BY));
+            x[t][c / 2] = __uint_as_float(pack16<false>(q.x, q.y));
           }
         }
         settle();
@@ -801,7 +809,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
         const float m0 = S.ref[0][row], m1 = S.ref[1][row], m = fmaxf(m0, m1), w0 = ex2(m0 - m), w1 = ex2(m1 - m);
         const float s0 = (S.sum[0][0][row] + S.sum[0][1][row]) + (S.sum[0][2][row] + S.sum[0][3][row]);
         const float s1 = (S.sum[1][0][row] + S.sum[1][1][row]) + (S.sum[1][2][row] + S.sum[1][3][row]);
-        const float total = s0 * w0 + s1 * w1, inv = !whole ? 1.f : total == 0.f ? 0.f : 1.f / total;
+        const float total = times_ex2(s0, m0 - m) + times_ex2(s1, m1 - m);
+        const float inv = !whole ? A8_MORE_BY : total == 0.f ? 0.f : A8_MORE_BY / total;
         S.weight[row] = make_float2((grp ? w1 : w0) * inv, (grp ? w0 : w1) * inv);
         if (whole) {
           const int tok = row / a.g;
@@ -884,7 +893,7 @@ cudaError_t launch(const AttnArgs &a, void *ws, cudaStream_t s) {
   const Pieces p = pieces_of(ws, blocks, R, DP);
   attention8_decode_kernel<R, DP, BF16><<<blocks, A8_THREADS, smem, s>>>(a, p, tk, tv, rows, item_tiles(R, (int64_t)a.R * a.G, blocks));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_join<DP, BF16>(a, p, blocks, R, 1 << 20, s);
+  return launch_join<DP, BF16, true>(a, p, blocks, R, 1 << 20, s);
 }
 
 template <int R>

@@ -94,6 +94,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 2^d (d <= 0) as a product, of which the second is 1 unless 2^d is below what a float
+// holds; and x times 2^d.
+__device__ __forceinline__ float2 ex2_parts(float d) { return make_float2(ex2(fmaxf(d, -126.f)), ex2(fminf(d + 126.f, 0.f))); }
+__device__ __forceinline__ float times_ex2(float x, float d) {
+  const float2 f = ex2_parts(d);
+  return x * f.x * f.y;
+}
+
 // Column sums (MAX: maxima) over a warp of W = 16 or 32 values a lane: lane i
 // ends with column i mod W.  Each step sends away the half of the columns
 // that the lane will not own, so it takes W - 1 shuffles (and one more for
@@ -460,13 +468,16 @@ inline Pieces pieces_of(void *ws, int blocks, int rows, int dp) {
 // from a cold cache; with 2 to 4 pieces a row a shared form's warps idle: 17
 // requests of 3 to 666 tokens 76 us with a warp a row, 114 shared).
 constexpr int JOIN_WARPS = 8, JOIN_FEW = 8, JOIN_BLOCKS = 32;
-template <int DP, bool BF16>
+// APART: maxima are not the weights' own, so that a sum may be large for a
+// maximum far below the others (attention8_decode.cu).
+template <int DP, bool BF16, bool APART>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) attention_join_kernel(const AttnArgs a, const Pieces p, int rows, int tok) {
   __shared__ float2 part_stats[JOIN_WARPS];
   __shared__ float part_sums[JOIN_WARPS][DP];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = blockIdx.x, blocks = gridDim.x;
   constexpr int PER = DP / 32;
+  auto scaled = [](float x, float d, float f) { return APART ? times_ex2(x, d) : x * f; };  // a sum times f = 2^d
   const int4 w0 = p.what[2 * block], w1 = p.what[2 * block + 1];
   const int own = lane && block + lane < blocks ? p.what[2 * (block + lane)].w : PIECE_END;  // the lane's block's first piece
   auto begun = [](const int4 &w) { return (w.w & (PIECE_USED | PIECE_START | PIECE_END)) == (PIECE_USED | PIECE_START); };
@@ -501,9 +512,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attention_join_kernel(const A
       float to = fmaxf(m, st.x);
 #pragma unroll
       for (int i = 16; i > 0; i >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, i));
-      const float keep = ex2(m - to), f = ex2(st.x - to), lf = st.y * f;
+      const float keep = ex2(m - to), f = ex2(st.x - to), lf = scaled(st.y, st.x - to, f);
+      l = scaled(l, m - to, keep);
       m = to;
-      l *= keep;
 #pragma unroll
       for (int i = 0; i < PER; ++i) o[i] *= keep;
       const int k = min(32, mine - i0);
@@ -529,7 +540,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attention_join_kernel(const A
         for (int v = 1; v < JOIN_WARPS; ++v) {
           const float2 st = part_stats[v];
           const float to = fmaxf(m, st.x), keep = ex2(m - to), f = ex2(st.x - to);
-          l = l * keep + st.y * f;
+          l = scaled(l, m - to, keep) + scaled(st.y, st.x - to, f);
 #pragma unroll
           for (int i = 0; i < PER; ++i) o[i] = o[i] * keep + part_sums[v][PER * lane + i] * f;
           m = to;
@@ -550,7 +561,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attention_join_kernel(const A
 }
 
 // Behind an attention kernel of `blocks` blocks; its set-up overlaps that kernel's end.
-template <int DP, bool BF16>
+template <int DP, bool BF16, bool APART = false>
 cudaError_t launch_join(const AttnArgs &a, const Pieces &p, int blocks, int rows, int tok, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks, std::min(rows, JOIN_BLOCKS));
@@ -561,7 +572,7 @@ cudaError_t launch_join(const AttnArgs &a, const Pieces &p, int blocks, int rows
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, BF16>, a, p, rows, tok);
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, BF16, APART>, a, p, rows, tok);
 }
 
 // The keys or values as a 4-D map {element, row of a page, head, page} with

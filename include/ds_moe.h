@@ -654,7 +654,9 @@ int ds_moe_kv8_append(const ds_moe_attn_shape *shape, const ds_moe_kv8_cache *ca
  *       sums of e4m3 numbers (exact down to 2^-22 of a row's largest element in
  *       bf16, 2^-27 in fp16), weights times their values' scales as sums of
  *       e5m2 numbers (fp16, for bf16 cut to 9 bits: off by 2^-11, 2^-9, or by
- *       2^-30 of the row's largest)
+ *       2^-30 of the row's largest); the weights' own sum, and lse, in fp32
+ *       whatever the values' scales are (where those are 2^120 apart, without
+ *       weights below 2^-35 of the largest)
  *   DS_ATTN_CHUNK: e4m3 * scale rounded to dtype (exact in bf16 where the scale is a power
  *       of two; in fp16 values beyond 65504 become 65504), the rest as in
  *       ds_moe_paged_attention
