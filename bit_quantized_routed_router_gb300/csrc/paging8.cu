@@ -42,6 +42,16 @@ __device__ __forceinline__ float scale_for(float most) {
 
 __device__ __forceinline__ float finite_or_nan(float x) { return fabsf(x) <= 3.402823466e38f ? x : __uint_as_float(0x7FFFFFFFu); }
 
+// A request's rows at the positions that its lengths give them, whether the table
+// and T reach so far or not: a token that has no place must not move the others
+// onto what is there already.
+__device__ __forceinline__ Span append_span(const Append8Args &a, int r, bool &bad) {
+  const RawSpan w = request_raw(a.cu, a.seq, r);
+  Span s = request_span(w, a.T, a.max_new, a.max_seq, bad);
+  s.pos0 = (int)max((int64_t)w.seq - w.c1 + s.t0, -((int64_t)1 << 25));  // (T is 2^24 at most: further back, none is at 0)
+  return s;
+}
+
 // A unit's elements as e4m3.  (Infinities only where `odd` says that there are
 // some: the conversion would make them 448.)
 template <int W>
@@ -103,7 +113,7 @@ __global__ void __launch_bounds__(A8_WARPS * 32, 4) kv8_append_kernel(const __gr
     const int part = (int)(w - group * a.y_queries);
     const int64_t t = group * lanes.rows + lanes.row;
     if (group >= a.groups || lanes.row < 0 || t >= a.T) return;
-    const Span s = request_span(a.cu, a.seq, request_of((int)t), a.T, a.max_new, a.max_seq, bad);
+    const Span s = append_span(a, request_of((int)t), bad);
     const int i = (int)t - s.t0;
     if (i < 0 || i >= s.n || s.pos0 + i < 0) return;
     for (int unit = lanes.unit; unit < units; unit += 32)
@@ -116,24 +126,26 @@ __global__ void __launch_bounds__(A8_WARPS * 32, 4) kv8_append_kernel(const __gr
   // ------------------------------------------------------------------ runs --
   const int64_t x = run_block / (unsigned)a.y_runs;
   const int row = (int)(run_block - x * a.y_runs) * A8_WARPS + warp;  // of the 2 G rows of heads
-  int r, t, pos;  // request, first token of the run and its position
+  int r, t;    // request, first token of the run
+  int64_t at;  // and its position
   Span s;
   if (a.per_request) {
     r = (int)(x / a.per_request);
     const int j = (int)(x - (int64_t)r * a.per_request);
-    s = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
+    s = append_span(a, r, bad);
     const int p0 = max(s.pos0, 0);
-    pos = j ? (int)min(((int64_t)p0 / a.block + j) * a.block, (int64_t)1 << 30) : p0;
-    t = s.t0 + (pos - s.pos0);
+    at = j ? (int64_t)(p0 / a.block + j) * a.block : p0;
+    t = s.t0 + (int)(at - s.pos0);
   } else {
     t = (int)x;
     r = request_of(t);
-    s = request_span(a.cu, a.seq, r, a.T, a.max_new, a.max_seq, bad);
-    pos = s.pos0 + t - s.t0;
-    if (t < s.t0 || pos < 0 || (pos % a.block && t > s.t0 && pos > 0)) t = a.T;  // does not begin a run
+    s = append_span(a, r, bad);
+    at = (int64_t)s.pos0 + t - s.t0;
+    if (t < s.t0 || at < 0 || (t > s.t0 && at % a.block)) t = a.T;  // does not begin a run
   }
   if (bad && row == 0 && lane == 0) flag(a.status, ST_PAGING);
-  if (t >= s.t0 + s.n) return;
+  if (t >= s.t0 + s.n || at >= a.max_seq) return;
+  const int pos = (int)at;
   const int in_block = pos % a.block, n = min(a.block - in_block, s.t0 + s.n - t);
   const int col = pos / a.page, page = a.table[r * a.table_stride + col];  // (under way while the elements are)
   const bool value = row >= a.G;

@@ -628,7 +628,7 @@ typedef struct {
  * block_table, cu_new and seq_lens as ds_moe_page_map writes them: token i of
  * a request's n is at position seq_len - n + i.  (A token before position 0
  * has no place and is left out, its queries too; so are tokens beyond max_new, which are
- * reported.)  With `rope` the keys are rotated first, and q's rows where they
+ * reported, as are those beyond the table's columns, which have no place.)  With `rope` the keys are rotated first, and q's rows where they
  * are given (q needs rope); q is rotated also where a token has no page.
  * The scale of a block and head is a power of two, the least (from 2^-60 to
  * 2^60) that brings the largest of its new elements to 448 or below.  Where
