@@ -193,7 +193,7 @@ extern "C" {
 
 int ds_moe_attention_path(const ds_moe_attn_shape *shape, const ds_moe_kv_cache *cache, const void *q,
                           int64_t q_stride, int32_t max_new) {
-  if (check_attn_shape(shape, nullptr, 0) || check_kv_cache(shape, cache, nullptr, 0) || max_new < 0 || q_stride < 0)
+  if (check_attn_shape(shape, nullptr, 0) || check_kv_cache(shape, cache, false, nullptr, 0) || max_new < 0 || q_stride < 0)
     return DS_ERR_INVALID_ARG;
   return path_of(*shape, *cache, q, q_stride, 2, max_new);
 }
@@ -218,7 +218,7 @@ int ds_moe_paged_attention(const ds_moe_attn_shape *shape, const ds_moe_kv_cache
                            void *stream, char *err, size_t errlen) {
   int rc = check_attn_shape(shape, err, errlen);
   if (rc) return rc;
-  if ((rc = check_kv_cache(shape, cache, err, errlen))) return rc;
+  if ((rc = check_kv_cache(shape, cache, false, err, errlen))) return rc;
   size_t need = 0;
   if ((rc = ds_moe_attention_workspace_bytes(shape, n_requests, T, max_new, &need, err, errlen))) return rc;
   AttnArgs a{};

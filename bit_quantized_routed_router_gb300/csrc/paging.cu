@@ -286,7 +286,7 @@ int ds_moe_kv_append(const ds_moe_attn_shape *shape, const ds_moe_kv_cache *cach
                      void *stream, char *err, size_t errlen) {
   int rc = check_attn_shape(shape, err, errlen);
   if (rc) return rc;
-  if ((rc = check_kv_cache(shape, cache, err, errlen))) return rc;
+  if ((rc = check_kv_cache(shape, cache, true, err, errlen))) return rc;
   if (T < 0 || T > (1 << 24)) return fail(err, errlen, DS_ERR_INVALID_ARG, "T=%lld out of range", (long long)T);
   if (T == 0) return DS_OK;
   if (!k_new || !v_new || !slots) return fail(err, errlen, DS_ERR_INVALID_ARG, "k_new, v_new and slots are required");

@@ -184,7 +184,7 @@ int ds_moe_kv_append_rotary(const ds_moe_attn_shape *shape, const ds_moe_kv_cach
                             void *stream, char *err, size_t errlen) {
   int rc = check_attn_shape(shape, err, errlen);
   if (rc) return rc;
-  if ((rc = check_kv_cache(shape, cache, err, errlen))) return rc;
+  if ((rc = check_kv_cache(shape, cache, true, err, errlen))) return rc;
   const int D = shape->head_dim, G = shape->n_head_kv;
   if ((rc = check_rope(rope, D, err, errlen))) return rc;
   if (T < 0 || T > (1 << 24)) return fail(err, errlen, DS_ERR_INVALID_ARG, "T=%lld out of range", (long long)T);

@@ -26,21 +26,6 @@ inline int check_attn_shape(const ds_moe_attn_shape *s, char *err, size_t errlen
   return DS_OK;
 }
 
-inline int check_kv_cache(const ds_moe_attn_shape *s, const ds_moe_kv_cache *c, char *err, size_t errlen) {
-  if (!c) return fail(err, errlen, DS_ERR_INVALID_ARG, "cache is NULL");
-  if (c->n_pages < 0 || c->n_pages > INT32_MAX) return fail(err, errlen, DS_ERR_INVALID_ARG, "n_pages out of range");
-  if (c->n_pages && (!c->k || !c->v)) return fail(err, errlen, DS_ERR_INVALID_ARG, "cache k and v are required");
-  if (!aligned(c->k, 2) || !aligned(c->v, 2))
-    return fail(err, errlen, DS_ERR_INVALID_ARG, "cache k and v must be aligned to their elements");
-  if (c->page_stride < 0 || c->row_stride < 0 || c->head_stride < 0)
-    return fail(err, errlen, DS_ERR_INVALID_ARG, "negative cache stride");
-  // rows that overlap would make an append's result depend on its order
-  if ((s->page_size > 1 && c->row_stride < s->head_dim) || (s->n_head_kv > 1 && c->head_stride < s->head_dim) ||
-      (c->n_pages > 1 && c->page_stride < s->head_dim))
-    return fail(err, errlen, DS_ERR_INVALID_ARG, "cache strides are smaller than head_dim");
-  return DS_OK;
-}
-
 // Whether blocks of `width` elements at all multiples, up to n[i] - 1 of them, of
 // K strides are apart from one another: each stride steps over all that the smaller
 // ones span.
@@ -56,6 +41,23 @@ inline bool apart(int64_t width, const int64_t (&n)[K], const int64_t (&stride)[
     span += (double)stride[i] * (double)(n[i] - 1);
   }
   return true;
+}
+
+inline int check_kv_cache(const ds_moe_attn_shape *s, const ds_moe_kv_cache *c, bool writes, char *err, size_t errlen) {
+  if (!c) return fail(err, errlen, DS_ERR_INVALID_ARG, "cache is NULL");
+  if (c->n_pages < 0 || c->n_pages > INT32_MAX) return fail(err, errlen, DS_ERR_INVALID_ARG, "n_pages out of range");
+  if (c->n_pages && (!c->k || !c->v)) return fail(err, errlen, DS_ERR_INVALID_ARG, "cache k and v are required");
+  if (!aligned(c->k, 2) || !aligned(c->v, 2))
+    return fail(err, errlen, DS_ERR_INVALID_ARG, "cache k and v must be aligned to their elements");
+  if (c->page_stride < 0 || c->row_stride < 0 || c->head_stride < 0)
+    return fail(err, errlen, DS_ERR_INVALID_ARG, "negative cache stride");
+  if ((s->page_size > 1 && c->row_stride < s->head_dim) || (s->n_head_kv > 1 && c->head_stride < s->head_dim) ||
+      (c->n_pages > 1 && c->page_stride < s->head_dim))
+    return fail(err, errlen, DS_ERR_INVALID_ARG, "cache strides are smaller than head_dim");
+  // rows that overlap would make an append's result depend on its order
+  if (writes && !apart<3>(s->head_dim, {c->n_pages, s->page_size, s->n_head_kv}, {c->page_stride, c->row_stride, c->head_stride}))
+    return fail(err, errlen, DS_ERR_INVALID_ARG, "rows of the cache overlap");
+  return DS_OK;
 }
 
 // Rows of one request: its tokens t0 .. t0 + n - 1, whose first is at

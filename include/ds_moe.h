@@ -435,7 +435,9 @@ typedef struct {
  * elements, the last axis dense.  Any order of the axes is fine (pages of
  * rows or of heads; both in one buffer).  The tensor-core attention wants the
  * bases (and q) 16-byte aligned, the strides, head_dim and page_size multiples
- * of 8, and at most 128 query heads a key head; others run on CUDA cores. */
+ * of 8, and at most 128 query heads a key head; others run on CUDA cores.
+ * An append refuses rows that overlap: each stride has to step over all that
+ * the smaller ones span. */
 typedef struct {
   void *k, *v;
   int64_t n_pages;

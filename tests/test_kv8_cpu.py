@@ -227,3 +227,28 @@ def test_binding_refuses(L, monkeypatch):
         with pytest.raises(ValueError):
             bad()
     assert len(called) == 6
+
+
+@pytest.mark.parametrize("kw", [dict(row_stride=128), dict(page_stride=16 * 8 * 128 - 1), dict(head_stride=8 * 128, row_stride=8 * 128),
+                                dict(page_stride=128, row_stride=8 * 128, n_pages=9), dict(row_stride=8 * 128 - 1)])
+def test_16_bit_appends_refuse_rows_that_overlap(L, kw):
+    """Where a row of one head is a row of another, or of another page, what an append leaves would depend on its order;
+    attention may read such a cache."""
+    sh, kv = shape(), cache(**kw)
+    err = ctypes.create_string_buffer(200)
+    assert L.ds_moe_kv_append(ctypes.byref(sh), ctypes.byref(kv), P, P, 1024, 128, P, 2, None, err, 200) == ARG and b"overlap" in err.value
+    err = ctypes.create_string_buffer(200)
+    assert L.ds_moe_kv_append_rotary(ctypes.byref(sh), ctypes.byref(kv), ctypes.byref(rope()), P, P, 1024, 128, None, P, P, 2, None, err,
+                                     200) == ARG and b"overlap" in err.value
+    a = [P, 4, 4, P, 32 * 128, 0, P, P, 2, 2, P, 32 * 128, None, P, 1 << 40]
+    assert L.ds_moe_paged_attention(ctypes.byref(sh), ctypes.byref(kv), *a, None, None, 0) == OK
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(row_stride=128, head_stride=16 * 128), dict(page_stride=2 * 16 * 8 * 128),
+                                dict(row_stride=10 * 8 * 128, page_stride=8 * 128), dict(row_stride=8 * 136, head_stride=136, page_stride=16 * 8 * 136),
+                                dict(n_pages=1, page_stride=0)])
+def test_16_bit_appends_take_any_order_of_the_axes(L, kw):
+    """(Refused for its rows' address, which is looked at behind the cache: nothing runs.)"""
+    err = ctypes.create_string_buffer(200)
+    assert L.ds_moe_kv_append(ctypes.byref(shape()), ctypes.byref(cache(**kw)), P + 1, P, 1024, 128, P, 2, None, err, 200) == ARG
+    assert b"aligned" in err.value
