@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(A8_WARPS * 32, 4) kv8_append_kernel(const __gr
       }
     }
   }
+  __syncwarp();  // (every lane has read the old scale)
   if (some && lane == 0) *scale_at = scale;
   if (once && !odd) kept([&](const float (&v)[2 * W], int i) { store8<W>(dst + i * a.rs, mine, v, by, false); });
   else visit(STORE);
