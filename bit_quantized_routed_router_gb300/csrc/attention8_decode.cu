@@ -139,8 +139,7 @@ __device__ __noinline__ bool copy_step(const AttnArgs &a, const StepRuns now, ui
 
 template <int W>
 __device__ __forceinline__ void tmem_ldw(uint32_t t, float *v) {
-  if (W == 4) tmem_ld4(t, v);
-  else if (W == 8) tmem_ld8(t, v);
+  if (W == 8) tmem_ld8(t, v);
   else if (W == 16) tmem_ld16(t, v);
   else tmem_ld32(t, v);
 }
