@@ -35,12 +35,13 @@
 // cache, and the kernel's size counts as much as its instructions do: what happens
 // once a segment is rolled or out of line, and both copying warps run one code.
 //
-// Measured (on the one of several cards where it is slowest, in brackets): 64
-// requests of 217 to 8138 keys, 32 heads over 8 of 128, bf16, 99 us (108), 82 % of
-// the copy bandwidth (75), with 8 to 16 rows a key head 118 (121), with 17 to 32
-// 163 (163); 3 requests of 68 to 93 thousand keys, 64 heads over 8, pages of 16
-// rows, fp16, 93 us (99); the same over a 16-bit cache 177 and 165.  29 requests
-// of 1 to 4 tokens with 7 query heads a key head of 64, 36 us.  Few-row calls
+// Measured (of several cards, the fastest and the slowest): 64
+// requests of 217 to 8138 keys, 32 heads over 8 of 128, bf16, 99 to 108 us, 82 to 75 % of
+// the copy bandwidth, with 16 rows a key head 118 (fp16 130), with 32 170 (184);
+// 3 requests of 68 to 93 thousand keys, 64 heads over 8, pages of 16
+// rows, fp16, 92 to 100 us; the same over a 16-bit cache 177 and 165.  29 requests
+// of 1 to 4 tokens with 7 query heads a key head of 64, 36 us.  (The room for the sum
+// costs nothing up to 8 rows, 1 % with 16 and 32, in fp16 4 %.)  Few-row calls
 // wait for memory: 128-byte rows of a head, as the 16-bit kernel's 256-byte ones.
 // More rows cost the softmax threads their exponentials and the cut of the weights.
 #include "attention_tc.cuh"

@@ -9,7 +9,7 @@ namespace {
 
 constexpr int A8_WARPS = 8;
 constexpr int A8_ROWS = 64;  // tokens whose angles a block holds at a time
-constexpr int A8_KEEP = 4;   // units of a lane that stay in registers
+constexpr int A8_KEEP = 4;   // units of a lane that are kept
 
 struct Append8Args {
   Rope rope;
@@ -79,12 +79,13 @@ __device__ __forceinline__ void store8(uint8_t *head, const Unit &u, const float
 // A run is the new tokens of one block of a request.  A block of threads takes
 // a run under eight of the 2 G rows of heads (keys, then values), a warp each:
 // it finds the run's largest element, from it the scale, and then quantises;
-// up to A8_KEEP tokens a lane (16 of head_dim 128 a warp) stay in registers in
-// between, longer runs are read twice.  The tokens' angles are computed by the
+// up to A8_KEEP tokens a lane (16 of head_dim 128 a warp) are kept in
+// between, longer runs are read twice.  (Four blocks an SM leave 64 registers, of which
+// the kernels for 16-byte loads spill 184 to 272 bytes a thread.)  The tokens' angles are computed by the
 // whole block into shared memory.  Queries are rotated by further blocks of
 // the same launch, as in rotary.cu.  15,156 tokens of 13 prompts, 32 query and
 // 8 key heads of 128, blocks of 16 tokens, fp16: 70 us, 72 % of the copy
-// bandwidth; the runs alone are 28 us, a third of it, as each waits in turn for
+// bandwidth; the runs alone are 28 to 31 us, under half of it, as each waits in turn for
 // lengths, page, elements and old scale, so queries' blocks are mixed with
 // them.  64 single tokens: 4.5 us in a graph.
 template <int W, bool INTER, bool BF16>

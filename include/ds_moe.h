@@ -475,7 +475,8 @@ int ds_moe_attention_workspace_bytes(const ds_moe_attn_shape *shape, int32_t n_r
  * products are held in fp32; on the tensor cores the probabilities are rounded
  * to dtype for the second product (off by at most half a unit in the last place
  * each; in fp16, those below 2^-21 of the row's largest by 2^-32 of it).  A page id
- * outside the cache counts as a page of zeros, and is reported.
+ * outside the cache counts as a page of zeros, and is reported; so is a sequence
+ * longer than the table's columns, which counts as ending with them.
  * T == 0 or n_requests == 0 is a no-op.  Workspace: 256-byte aligned, scratch.
  * The result does not depend on the order in which blocks run. */
 int ds_moe_paged_attention(const ds_moe_attn_shape *shape, const ds_moe_kv_cache *cache, const int32_t *block_table,
